@@ -8,6 +8,10 @@ is no CPU fallback: if the shared library is missing, every call raises ``QmmUna
     y = qmm(x, packed, scales, biases, bits=4, group=64)       # x: [M,K], y: [M,N], M <= 64
     w_hat = dequantize(packed, scales, biases, K, bits=4, group=64, dtype=torch.float16)
 
+A paged K/V cache in the same format at 4 bits and attention over it are in ``kv.py`` (``KVCache``,
+``kv_append``, ``kv_attention``, ``kv_gather``, ``kv_copy_pages``, ``kv_compact`` and the bookkeeping
+of a batch of sequences, ``KVSequences``); all are names of this package too.
+
 Operation (MLX issue #4720, "To Reproduce": quantized_matmul(x, *w, transpose=True)):
 y[m,n] = sum_k x[m,k] * (s[n,k/g] * q[n,k] + b[n,k/g]).
 """
@@ -51,6 +55,21 @@ class Plan(ctypes.Structure):
 class Item(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("biases", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("N", ctypes.c_int64)]
+
+
+class CacheDesc(ctypes.Structure):
+    """qmm_kv_cache of the C ABI."""
+    _fields_ = [("k_packed", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("k_biases", ctypes.c_void_p),
+                ("v_packed", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("v_biases", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32), ("bits", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class SeqsDesc(ctypes.Structure):
+    """qmm_kv_seqs of the C ABI."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p), ("seqs", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
 
 
 _lib = None
@@ -97,6 +116,17 @@ def lib() -> ctypes.CDLL:
     L.qmm_nt.restype = I
     L.qmm_batched.argtypes = [P, I64, P, I64, P, P, I64, P, I64, I64, I64, I64, I64, I, I, U, I, P]
     L.qmm_batched.restype = I
+    F, C, S = ctypes.c_float, ctypes.POINTER(CacheDesc), ctypes.POINTER(SeqsDesc)
+    L.qmm_kv_append.argtypes = [C, P, I64, I64, P, I64, I64, S, P, I64, U, P]
+    L.qmm_kv_append.restype = I
+    L.qmm_kv_gather.argtypes = [C, S, P, I64, P, I64, I64, P, I64, I64, U, P]
+    L.qmm_kv_gather.restype = I
+    L.qmm_kv_copy_pages.argtypes = [C, P, P, I64, P]
+    L.qmm_kv_copy_pages.restype = I
+    L.qmm_kv_compact.argtypes = [C, S, P, P, I64, P]
+    L.qmm_kv_compact.restype = I
+    L.qmm_kv_attention.argtypes = [C, P, I64, I64, P, I64, I64, P, S, P, I64, I, F, I64, P, U, P]
+    L.qmm_kv_attention.restype = I
     _lib = L
     return L
 
@@ -418,3 +448,7 @@ class QuantizedWeight:
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, plan: Plan | None = None):
         return qmm(x, self.packed, self.scales, self.biases, self.bits, self.group, out=out, plan=plan)
+
+
+from .kv import (KVCache, KVSequences, kv_append, kv_attention, kv_compact, kv_copy_pages,  # noqa: E402
+                 kv_gather)

@@ -43,8 +43,8 @@ def _stale(srcs, target) -> bool:
 
 def build_call_module(force: bool = False) -> str:
     """gcc the CPython hand-off module (plain C against the interpreter's headers)."""
-    if not force and os.path.exists(CALL_LIB) and os.path.getmtime(CALL_LIB) >= max(
-            os.path.getmtime(CALL_SRC), os.path.getmtime(__file__)):
+    deps = (CALL_SRC, os.path.join(HERE, "..", "include", "qmm.h"), __file__)
+    if not force and os.path.exists(CALL_LIB) and os.path.getmtime(CALL_LIB) >= max(map(os.path.getmtime, deps)):
         return CALL_LIB
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if not cc:

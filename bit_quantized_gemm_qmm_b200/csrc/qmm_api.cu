@@ -15,7 +15,8 @@ namespace {
 
 thread_local char g_last_error[512] = "";
 
-qmm_status fail(qmm_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
 qmm_status fail(qmm_status s, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -24,9 +25,13 @@ qmm_status fail(qmm_status s, const char* fmt, ...) {
     return s;
 }
 
+namespace {
+
 qmm_status cuda_fail(cudaError_t e, const char* what) {
     return fail(QMM_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+}  // namespace
 
 // A launch helper's result: cudaErrorNotSupported means the kernel turned the shape or the
 // arrays down before launching anything (for example a tensor map that cannot be encoded).
@@ -37,6 +42,8 @@ qmm_status launch_result(cudaError_t e, const char* what) {
                     "scratch size); nothing was launched", what);
     return cuda_fail(e, what);
 }
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -649,7 +656,12 @@ qmm_status qmm_device_errors(uint32_t* bits) {
     unsigned z = 0;
     e = sk_read_and_clear_errors(&z);
     if (e != cudaSuccess) return cuda_fail(e, "qmm_device_errors");
-    *bits = v | w | z;
+    unsigned kv = 0, at = 0;
+    e = kv_read_and_clear_errors(&kv);
+    if (e != cudaSuccess) return cuda_fail(e, "qmm_device_errors");
+    e = attn_read_and_clear_errors(&at);
+    if (e != cudaSuccess) return cuda_fail(e, "qmm_device_errors");
+    *bits = v | w | z | kv | at;
     return QMM_OK;
 }
 

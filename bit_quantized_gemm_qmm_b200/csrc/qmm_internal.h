@@ -138,6 +138,50 @@ cudaError_t launch_stream_items(const QmmArgs& a, const SkItem* items, int nitem
                                 cudaStream_t stream);
 cudaError_t stream_read_and_clear_errors(unsigned* out);
 
+// Records the calling thread's failure (qmm_last_error) and returns its status; a launch's result.
+qmm_status fail(qmm_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+qmm_status launch_result(cudaError_t e, const char* what);
+
+// The paged K/V cache's other operators (qmm_kv.cu).  Sizes are validated; strides in elements.
+struct KvArgs {
+    uint32_t *kc, *vc;                     // codes [pages, kv_heads, page, dim / 8] words
+    uint16_t *ks, *kb, *vs, *vb;           // [pages, kv_heads, page, dim / group]
+    const uint16_t *k, *v;                 // append: dense rows in
+    uint16_t *k_out, *v_out;               // gather: dense rows out
+    int64_t k_ts, k_hs, v_ts, v_hs;        // strides of either, token and head
+    const int32_t *table, *at, *cu;        // at: lengths (append) or first positions (gather, compact)
+    int64_t table_stride, pages;
+    int page, capacity;                    // positions a page, and that a table row can name
+    int dim, group, seqs, tokens, kv_heads;
+    int is_bf16, vec;                      // vec: append's rows are 16-byte aligned
+};
+cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_gather(const KvArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_copy_pages(const KvArgs& a, const int32_t* src, const int32_t* dst, int pairs, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvArgs& a, const int32_t* keep, int kept, cudaStream_t stream);
+cudaError_t kv_read_and_clear_errors(unsigned* out);
+
+// Attention over the paged K/V cache (qmm_attn.cu).  Sizes are validated; strides in elements.
+struct AttnArgs {
+    const uint8_t *kc, *vc;                // codes [pages, kv_heads, page, head_dim / 2] bytes
+    const uint16_t *ks, *kb, *vs, *vb;     // [pages, kv_heads, page, head_dim / group]
+    const uint16_t* q;
+    uint16_t* o;
+    float* lse;                            // [tokens, heads] or null
+    int64_t q_ts, q_hs, o_ts, o_hs;
+    const int32_t *table, *lens, *cu;
+    const int64_t* tree;                   // [tokens] or null
+    int64_t table_stride;
+    float* part;                           // partial sums (set by the launch)
+    int64_t pages;
+    int page, capacity;                    // positions a page, and that a table row can name
+    int seqs, tokens, kv_heads, group_heads, window;
+    float scale_log2;                      // scale * log2(e)
+    int is_bf16, q_vec;                    // q_vec: rows of q are 16-byte aligned
+};
+cudaError_t launch_attn(const AttnArgs& a, int head_dim, int group, cudaStream_t stream);
+cudaError_t attn_read_and_clear_errors(unsigned* out);
+
 // 2-D tiled TMA descriptor over a row-major [outer, inner] array (row pitch inner*esize bytes).
 bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void* base, uint64_t inner,
                  uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);

@@ -270,12 +270,122 @@ qmm_status qmm_batched(const void* x, int64_t x_stride, const uint32_t* packed, 
                        int64_t y_stride, int64_t batch, int64_t M, int64_t N, int64_t K, int bits,
                        int group, qmm_dtype dtype, int transpose, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * A paged K/V cache in the same affine format at 4 bits, and attention over it: what a decoder
+ * does between the q/k/v and the o projection.  Row (page, head, position in the page) of each
+ * array is one K or V vector of head_dim values, quantized along itself by qmm_quantize's scheme;
+ * a page is contiguous in every array.  Attention is then qmm's form (scores, along K's rows) and
+ * qmm_nt's (sums over V's rows) with a softmax between them, in one pass over the cache.
+ *
+ * A call covers `seqs` sequences.  Position p of sequence b is row p % page_size of page
+ * page_table[b * table_stride + p / page_size]; its rows of the token axis (q, k, v, o and the
+ * like) are [cu_tokens[b], cu_tokens[b + 1]).  Page tables, lengths and offsets are read on the
+ * device, in stream order, so that a captured graph may be replayed with other contents.  Rows of
+ * the token axis in front of cu_tokens[0] or from cu_tokens[seqs] on belong to no sequence and
+ * are left as they are; offsets are clamped to [0, tokens].
+ *
+ * What only the device can see is checked there: a position beyond max_pages * page_size, a
+ * negative one, or a page outside [0, pages) is not accessed (append, copy and compact skip it,
+ * gather writes zeros, attention leaves it out) and sets bit 1 of qmm_device_errors().
+ */
+typedef struct {
+    uint32_t* k_packed;  /* [pages, kv_heads, page_size, head_dim/8]                         */
+    uint16_t* k_scales;  /* [pages, kv_heads, page_size, head_dim/group] fp16                */
+    uint16_t* k_biases;
+    uint32_t* v_packed;  /* V's, likewise.  All six 16-byte aligned, owned by the caller     */
+    uint16_t* v_scales;
+    uint16_t* v_biases;
+    int64_t pages;
+    int32_t page_size;   /* a multiple of 16 up to 1024                                      */
+    int32_t kv_heads;    /* 1..256                                                           */
+    int32_t head_dim;    /* 64, 128 or 256                                                   */
+    int32_t group;       /* 32, 64 or 128, dividing head_dim                                 */
+    int32_t bits;        /* 4                                                                */
+    int32_t reserved;
+} qmm_kv_cache;
+
+typedef struct {
+    const int32_t* page_table;  /* [seqs, table_stride], of which max_pages a row are read   */
+    const int32_t* cu_tokens;   /* [seqs + 1], not falling                                   */
+    int64_t seqs;               /* up to 65536                                               */
+    int64_t table_stride;
+    int64_t max_pages;
+} qmm_kv_seqs;
+
+/*
+ * qmm_kv_append -- quantizes the K and V rows of new tokens into the cache, bit for bit as
+ * qmm_quantize does.  lens[b] counts sequence b's tokens with the new ones, which are its last:
+ * row cu_tokens[b] + i is position lens[b] - (cu_tokens[b+1] - cu_tokens[b]) + i.  k and v are
+ * [tokens, kv_heads, head_dim] fp16/bf16 with the given strides (in elements; the last dimension is
+ * contiguous), 2-byte aligned; 16-byte aligned rows are read faster.  tokens up to 2^20.  A
+ * group that holds an infinity or a NaN, or whose scale or bias is beyond fp16, reads back as
+ * NaN.  Two rows of one call must not go to the same position of the same page.
+ */
+qmm_status qmm_kv_append(const qmm_kv_cache* cache, const void* k, int64_t k_token_stride,
+                         int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                         int64_t v_head_stride, const qmm_kv_seqs* seqs, const int32_t* lens,
+                         int64_t tokens, qmm_dtype dtype, void* stream);
+
+/*
+ * qmm_kv_gather -- reads rows back as qmm_dequantize does: row cu_tokens[b] + i of k and v
+ * ([tokens, kv_heads, head_dim], 16-byte aligned, strides multiples of 8 elements) becomes
+ * position starts[b] + i of sequence b.
+ */
+qmm_status qmm_kv_gather(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, const int32_t* starts,
+                         int64_t tokens, void* k, int64_t k_token_stride, int64_t k_head_stride,
+                         void* v, int64_t v_token_stride, int64_t v_head_stride, qmm_dtype dtype,
+                         void* stream);
+
+/*
+ * qmm_kv_copy_pages -- page dst[i] becomes a copy of page src[i], K and V, all heads, for i <
+ * pairs (up to 2^20): the partly filled last page of a forked sequence, a pool that is made
+ * dense.  Of pairs with the same dst the last one counts.  A page must not be one pair's src and
+ * another's dst: such a pair (the one that would read it) is skipped and sets bit 1 of
+ * qmm_device_errors().
+ */
+qmm_status qmm_kv_copy_pages(const qmm_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                             int64_t pairs, void* stream);
+
+/*
+ * qmm_kv_compact -- moves the rows of accepted draft tokens together: for j in
+ * [cu_tokens[b], cu_tokens[b+1]), position starts[b] + keep[j] of sequence b moves to position
+ * starts[b] + j - cu_tokens[b].  keep rises within a sequence and has `kept` entries in all.
+ * The page tables of the sequences must not share the pages that are written.
+ */
+qmm_status qmm_kv_compact(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, const int32_t* starts,
+                          const int32_t* keep, int64_t kept, void* stream);
+
+/*
+ * qmm_kv_attention -- o = softmax(scale * q K^T + mask) V over the cache, for any number of new
+ * tokens a sequence: one while decoding, a draft while verifying, a chunk of a prompt.
+ *   q, o   [tokens, heads, head_dim] fp16/bf16 with the given strides (elements); q 2-byte, o
+ *          8-byte aligned with strides multiples of 4.  Query head h reads K/V head
+ *          h / (heads / kv_heads); heads up to 256, a multiple of kv_heads.
+ *   lse    [tokens, heads] fp32, log sum exp(scale * q K^T + mask); may be null.
+ *   lens   tokens of each sequence with the new ones, which are its last (as in qmm_kv_append,
+ *          which comes first).  The token at position p sees positions <= p; with window > 0
+ *          only those > p - window.
+ *   tree   64-bit mask per row of the token axis, or null: a token then sees every position before
+ *          its sequence's new tokens and, of those, number j if bit j of its mask is set (those
+ *          past 64 are not seen).  Not together with a window.
+ * A row that sees nothing is zeros with lse = -infinity.  What a row does not see has no part
+ * in it, NaN included.  Arithmetic: codes enter the tensor cores exactly; scores, softmax and sums
+ * are fp32; each probability times V's scale is rounded once to fp16, q to fp16 relative to its
+ * row's largest value (exact unless 2^-24 below it), o once.  Results do not depend on timing.
+ * Uses the stream's workspace (as qmm).
+ */
+qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, void* o, int64_t o_token_stride,
+                            int64_t o_head_stride, float* lse, const qmm_kv_seqs* seqs,
+                            const int32_t* lens, int64_t tokens, int heads, float scale,
+                            int64_t window, const int64_t* tree, qmm_dtype dtype, void* stream);
+
 /* Read and clear the current device's kernel error word (synchronizes with the device).
  * Bit 0: a tensor-core kernel block gave up waiting on one of its pipeline barriers (a wait
  * that should finish in microseconds ran for about two seconds).  That block then dropped
  * its work, drained its own copies in flight, released its tensor memory and exited rather
- * than hang; its part of y is not valid.  Returns QMM_OK and *bits = 0 when nothing went
- * wrong. */
+ * than hang; its part of y is not valid.  Bit 1: a K/V cache operator met a page or position
+ * outside the cache (see there).  Returns QMM_OK and *bits = 0 when nothing went wrong. */
 qmm_status qmm_device_errors(uint32_t* bits);
 
 /* Static description of a status code. */
