@@ -10,12 +10,15 @@
 // (for V).  Both products run with the codes as the 16-row operand and 8 query rows as the
 // 8-column one (mma.sync m16n8k16):
 //   - K: ldmatrix gives lane (g, c) word c of row g, whose nibble pairs are two k indices; the
-//     group's fp32 sums are scaled by s afterwards, b enters as b * sum(Q over the group).
+//     group's fp32 sums are scaled by s afterwards.  b * sum(Q over the group) is one more MMA: b as
+//     it is, the sum as three fp16 terms.
 //   - V: ldmatrix.trans on the 16-bit units (four codes) of the rows gives lane (g, c) the unit
 //     g of rows 2c and 2c + 1 in one register, whose nibble pairs are two positions (k) of one
-//     d (row).  V's codes are centred (q - 8, one packed add a pair), and each group's P * s is
-//     rounded once to fp16: with centred codes that rounding weighs in with the spread of V and
-//     not with its distance from the bias.  b + 8s enters through fp32 sums of P * (b + 8s).
+//     d (row).  Each group's P * s is rounded once to fp16.  V's codes are centred (q - 8), so that
+//     this rounding weighs in with the spread of V and not with its distance from the bias: 8 times
+//     the sum of the rounded P * s is taken off at the end (one more MMA a group, of a constant),
+//     or, with many columns, each pair of codes by a packed add.  b + 8s enters through fp32 sums
+//     of P * (b + 8s).
 // The scores' layout (position by query) is the transpose of the second product's operand;
 // movmatrix turns the packed P * s round.
 //
@@ -24,10 +27,10 @@
 // of a large or NaN fp16 is bit 14) or x - ref reaches 60.  The reference is then put so that
 // the largest P * s of the tile is 2^-4.
 //
-// Work: units of 64 positions of one (sequence, K/V head, row tile) are dealt out evenly over
-// the resident blocks (qmm_kv_plan.h), whatever the lengths; a warp streams 16-position tiles of
-// its block's share through its own cp.async ring.  Items that several blocks share are summed
-// by a second small kernel in block order, so results do not depend on timing.
+// Work: units of 32 positions of one (sequence, K/V head, row tile) are dealt out evenly over
+// the resident blocks (qmm_kv_plan.h), whatever the lengths; a block's warps take them in turn, each
+// through its own cp.async ring.  Items that several blocks share are summed by the last of them to
+// arrive, in block order, so results do not depend on timing.
 #include <climits>
 #include <mutex>
 #include <type_traits>
@@ -77,6 +80,17 @@ __device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float half_lo(uint32_t v) { return __half2float(__ushort_as_half(uint16_t(v))); }
 __device__ __forceinline__ float half_hi(uint32_t v) { return __half2float(__ushort_as_half(uint16_t(v >> 16))); }
 
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
 // NG fp16 values of one row from shared memory, as floats.
 template <int NG>
 __device__ __forceinline__ void lds_halves(uint32_t addr, float (&f)[NG]) {
@@ -98,33 +112,40 @@ __device__ __forceinline__ void lds_halves(uint32_t addr, float (&f)[NG]) {
     }
 }
 
-// Shared-memory layout of an instance: per warp a ring of tiles (reused for the warp's partial
-// sums at the end of an item), then Q as MMA fragments and the rows' constants.
+// Shared-memory layout of an instance: per warp a ring of tiles of kAttnUnit positions (its first slots
+// hold the warp's partial sums at the end of an item), then Q as MMA fragments and the rows' constants.
 template <int D, int GRP, int NT>
 struct AttnFmt {
+    static constexpr int W = D == 256 || NT > 2 ? 4 : 6;  // warps a block; two blocks an SM
     static constexpr int NG = D / GRP;
-    static constexpr int CH = D / 32;              // 16-byte pieces (32 codes) of a row
+    static constexpr int CH = D / 32;                 // 16-byte pieces (32 codes) of a row
     static constexpr int ROWS = 8 * NT;
-    static constexpr int CODES = kAttnTile * D / 2;  // bytes of a tile's K (or V) codes
-    static constexpr int SB = kAttnTile * NG * 2;    // bytes of a tile's K scales (or biases, V's)
+    static constexpr int CODES = kAttnUnit * D / 2;   // bytes of a tile's K (or V) codes
+    static constexpr int SB = kAttnUnit * NG * 2;     // bytes of a tile's K scales (or biases, V's)
     static constexpr int TILE = 2 * CODES + 4 * SB;
-    static constexpr int RING = D == 256 ? 3 : 4;
-    static constexpr int OROW = D + 4;             // floats between rows of the partial sums
+    static constexpr int OROW = D + 4;                // floats between rows of the partial sums
     static constexpr int MERGE = ROWS * OROW * 4 + ROWS * 8;
-    static constexpr int WARP = RING * TILE > MERGE ? RING * TILE : (MERGE + 127) / 128 * 128;
-    static constexpr int QF = ROWS * D * 2;        // Q fragments
-    static constexpr int OFF_Q = kAttnWarps * WARP;
-    static constexpr int OFF_F = OFF_Q + QF;       // float per row: factor of the code sums
-    static constexpr int OFF_QB = OFF_F + ROWS * 4;       // float per row and group: factor of b
-    static constexpr int OFF_LIM = OFF_QB + ROWS * NG * 4;  // int per row: last position seen
-    static constexpr int OFF_BITS = (OFF_LIM + ROWS * 4 + 7) / 8 * 8;  // 64-bit mask per row
-    static constexpr int SMEM = OFF_BITS + ROWS * 8;
-    static constexpr int SLOT = ROWS * (D + 2);    // floats of one partial-sum slot
+    static constexpr int MS = (MERGE + TILE - 1) / TILE;  // ring slots under the partial sums
+    static constexpr int QF = ROWS * D * 2;           // Q fragments
+    static constexpr int CONSTS = ROWS * (4 + 4 + 8 + 8 * NG) + 16 + W * 2 * 96;
+    // the ring: four tiles, or as many as leave room for two blocks an SM
+    static constexpr int ROOM = 113 * 1024 - QF - CONSTS;
+    static constexpr int FIT = ROOM / (W * TILE);
+    static constexpr int RING = FIT > 4 ? 4 : FIT;
+    static_assert(RING >= 2 && RING >= MS, "ring too small");
+    static constexpr int WARP = RING * TILE;
+    static constexpr int OFF_Q = W * WARP;
+    static constexpr int OFF_F = OFF_Q + QF;          // float per row: factor of the sums
+    static constexpr int OFF_LIM = OFF_F + ROWS * 4;  // int per row: last position seen
+    static constexpr int OFF_BITS = OFF_LIM + ROWS * 4;   // 64-bit mask per row
+    static constexpr int OFF_QB = OFF_BITS + ROWS * 8;    // sum of Q over a group as three fp16 (and a zero), per row and group
+    static constexpr int OFF_LAST = OFF_QB + ROWS * NG * 8;
+    static constexpr int OFF_RUN = OFF_LAST + 16;     // per warp: this run and the next
+    static constexpr int SMEM = OFF_RUN + W * 2 * 96;
+    static constexpr int SLOT = ROWS * (D + 2);       // floats of one partial-sum slot
+    static constexpr int SUBS = NT == 1 && D * NG <= 256 ? 2 : 1;  // 16-position halves of a tile taken together
+    static constexpr bool SUMS = NT == 1 && NG <= 4;       // V's codes centred by sums of P * s, not one by one
 };
-
-__device__ __forceinline__ AttnSeq load_seq(const AttnArgs& a, int b, int rows) {
-    return attn_seq(a.cu[b], a.cu[b + 1], a.lens[b], a.tokens, a.capacity, a.group_heads, rows, a.window);
-}
 
 // Four values of an output row: sum / l, rounded once; with the first of them the row's lse.
 // A row that saw nothing (l = 0) is zeros and -infinity.
@@ -144,30 +165,36 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int row, int head,
             l == 0.f ? -INFINITY : (ref + lg2(l)) * 0.693147180559945309f;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
+__device__ __forceinline__ AttnSeq load_seq(const AttnArgs& a, int b, int rows) {
+    return attn_seq(a.cu[b], a.cu[b + 1], a.lens[b], a.tokens, a.capacity, a.group_heads, rows, a.window);
 }
 
-__device__ __forceinline__ int64_t all_units(const AttnArgs& a, int rows, int lane) {
-    int64_t sum = 0;
-    for (int b = lane; b < a.seqs; b += 32) sum += attn_seq_units(load_seq(a, b, rows), a.kv_heads);
-    return warp_sum64(sum);
+// Units and items of all sequences; false if offsets fall.
+__device__ __forceinline__ bool all_work(const AttnArgs& a, int rows, int lane, int* units, int* items) {
+    int u = 0, n = 0;
+    bool falls = false;
+    for (int b = lane; b < a.seqs; b += 32) {
+        const AttnSeq s = load_seq(a, b, rows);
+        falls |= s.falls;
+        u += attn_seq_units(s, a.kv_heads);
+        n += attn_seq_items(s, a.kv_heads);
+    }
+    *units = __reduce_add_sync(kFull, u);
+    *items = __reduce_add_sync(kFull, n);
+    return !__any_sync(kFull, falls);
 }
 
-// The sequence in which position x of the running sum of `weight` falls; *before = the sum of
-// those in front of it.
-template <class F>
-__device__ __forceinline__ int find_seq(int seqs, int64_t x, int lane, int64_t* before, F weight) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < seqs; b0 += 32) {
+// The sequence in which place x of the running sum of the sequences' weights falls (seqs if past the
+// end); *before = the sum of those in front of it.
+__device__ __forceinline__ int find_seq(const AttnArgs& a, const AttnPlan& p, int rows, int x, int lane, int* before) {
+    int base = 0;
+    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
         const int b = b0 + lane;
-        const int64_t w = b < seqs ? weight(b) : 0;
-        int64_t inc = w;
+        const int w = b < a.seqs ? attn_seq_weight(p, load_seq(a, b, rows), a.kv_heads) : 0;
+        int inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(kFull, inc, o);
+            const int u = __shfl_up_sync(kFull, inc, o);
             if (lane >= o) inc += u;
         }
         const unsigned past = __ballot_sync(kFull, base + inc > x);
@@ -178,24 +205,28 @@ __device__ __forceinline__ int find_seq(int seqs, int64_t x, int lane, int64_t* 
         }
         base += __shfl_sync(kFull, inc, 31);
     }
-    *before = base;
-    return seqs;
+    return a.seqs;
 }
 
-// One block's share of one item, and what its warps need of it.
+// One block's share of one item.  Kept in shared memory, a copy a warp; it is looked at once an item.
 struct Run {
-    int b, h, rt;      // sequence, K/V head, row tile
+    int row0, start, keys, units;  // of the sequence (AttnSeq)
+    int b, h;          // sequence, K/V head
     int u0, n;         // first unit of the item, units
     int row_lo, rows;  // first query row (of the sequence) and how many
     int lo, hi;        // positions that some row sees
     int full_lo, full_hi;  // positions [full_lo, full_hi) that every row sees
+    int t0;            // position of the first unit
+    int first;         // the item is the block's first
+    int c0, c1;        // the blocks that share the item
+    int x, before;     // place in the order of the blocks; weight of the sequences in front of b
 };
+static_assert(sizeof(Run) <= 96, "Run does not fit its place");
 
 template <int D, int GRP, int NT>
-__global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D == 256 && NT == 2 ? 2 : NT == 4 ? 2 : 3)
-    attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(const __grid_constant__ AttnArgs a) {
     using F = AttnFmt<D, GRP, NT>;
-    constexpr int NG = F::NG, CH = F::CH, R = F::ROWS;
+    constexpr int NG = F::NG, CH = F::CH, R = F::ROWS, W = F::W, SUBS = F::SUBS, THREADS = 32 * W;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t sbase = smem_addr(smem);
@@ -204,91 +235,176 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
     grid_dependency_wait();
     grid_dependents_launch();
 
-    const int64_t total = all_units(a, R, lane);
-    const int64_t shares = attn_shares(total, gridDim.x);
-    if (blockIdx.x >= shares) return;
-    int64_t x = attn_share(blockIdx.x, total, shares);
-    const int64_t x_end = attn_share(int64_t(blockIdx.x) + 1, total, shares);
-    int64_t before;
-    int b = find_seq(a.seqs, x, lane, &before, [&](int i) { return attn_seq_units(load_seq(a, i, R), a.kv_heads); });
+    AttnPlan pl;
+    int x_end;
+    Run* cur = reinterpret_cast<Run*>(smem + F::OFF_RUN + w * 192);
+    Run* next = cur + 1;
 
-    // per-lane constants of the tile copies: codes (16-byte piece i of a tile goes to row i / CH,
-    // piece i % CH, xor-swizzled so that eight rows' equal pieces fall into different banks)
+    // ---- the item at place x of the order of the blocks, in or after sequence b, and this block's share
+    auto plan = [&](Run* r, int x, int b, int before, bool first_item) {
+        AttnSeq s = load_seq(a, b, R);
+        int weight = attn_seq_weight(pl, s, a.kv_heads);
+        while (x >= before + weight) {
+            before += weight;
+            s = load_seq(a, ++b, R);
+            weight = attn_seq_weight(pl, s, a.kv_heads);
+        }
+        const AttnShare sh = attn_share(pl, s, x, x_end, before);
+        const int h = sh.item / s.rt, row_lo = (sh.item - h * s.rt) * R, nrows = s.n * a.group_heads;
+        const int rows = nrows - row_lo < R ? nrows - row_lo : R;
+        const int first = s.start + row_lo / a.group_heads, last = s.start + (row_lo + rows - 1) / a.group_heads;
+        int lo, hi;
+        attn_range(s, row_lo, row_lo + rows, a.group_heads, a.window, a.tree != nullptr, &lo, &hi);
+        if (lane == 0) {
+            r->row0 = s.row0, r->start = s.start, r->keys = s.keys, r->units = s.units;
+            r->b = b, r->h = h, r->u0 = sh.u0, r->n = sh.n;
+            r->row_lo = row_lo, r->rows = rows, r->lo = lo, r->hi = hi;
+            const int all = a.tree ? s.start : first + 1;
+            r->full_hi = all < s.keys ? all : s.keys;
+            r->full_lo = a.window > 0 && last >= a.window ? last - a.window + 1 : 0;
+            r->t0 = s.lo + kAttnUnit * sh.u0;
+            r->first = first_item;
+            r->c0 = sh.c0, r->c1 = sh.c1, r->x = x, r->before = before;
+        }
+        __syncwarp();
+        return s.start + s.n > a.capacity;  // the table cannot name all of its positions
+    };
+    bool bad;
+    {
+        int total, items, before = 0;
+        if (!all_work(a, R, lane, &total, &items)) {
+            if (blockIdx.x == 0 && tid == 0) atomicOr(&g_attn_errors, 2u);
+            return;
+        }
+        pl = attn_plan(total, items, gridDim.x, W);
+        const int x = pl.pieces ? int(blockIdx.x) : int(blockIdx.x) * pl.per;
+        x_end = pl.pieces ? x + 1 : x + pl.per < total ? x + pl.per : total;
+        const int b = find_seq(a, pl, R, x, lane, &before);
+        if (b >= a.seqs) return;
+        bad = plan(cur, x, b, before, true);
+    }
+
+    // ---- tile copies.  Codes: 16-byte piece p of a tile goes to row p / CH, piece p % CH, xor-swizzled
+    // so that eight rows' equal pieces fall into different banks.  A lane's pieces of 16 rows lie at
+    // fixed distances, in the cache and in the tile.
     auto swz = [](int row, int ch) { return row * (D / 2) + ((ch ^ ((row * (D / 2) >> 7) & (CH - 1))) << 4); };
-    constexpr int CPT = kAttnTile * CH / 32;  // 16-byte pieces of codes a lane copies, K and V each
-    constexpr int SPT = (8 * NG + 31) / 32;   // of scales and biases
-    bool first_item = true;
-    bool bad = false;
+    constexpr int CPT = CH / 2;                 // pieces of codes a lane copies of a half tile, K and V each
+    constexpr int SPT = NG >= 2 ? NG / 2 : 1;   // pieces of scales and biases a lane copies of a tile
+    uint32_t cdst[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) cdst[i] = ring + swz((i * 32 + lane) / CH, (i * 32 + lane) % CH);
+    const bool s_on = 16 * NG >= 32 || lane < 16 * NG;
+    const int s_sub = (lane % (4 * NG)) / (2 * NG);
+    const uint8_t* ssrc[SPT];
+#pragma unroll
+    for (int i = 0; i < SPT; ++i) {
+        const int p = i * 32 + (s_on ? lane : 0), arr = p / (4 * NG);
+        ssrc[i] = reinterpret_cast<const uint8_t*>(arr == 0 ? a.ks : arr == 1 ? a.kb : arr == 2 ? a.vs : a.vb) + p % (2 * NG) * 16;
+    }
+    const uint8_t* const ksrc = a.kc + lane * 16;
+    const uint8_t* const vsrc = a.vc + lane * 16;
 
-    while (x < x_end) {
-        // ---- the item and this block's part of it
-        const AttnSeq s = load_seq(a, b, R);
-        const int64_t wb = attn_seq_units(s, a.kv_heads);
-        if (x >= before + wb) {
-            before += wb;
-            ++b;
-            continue;
+    int t0 = 0, j0 = 0, j1 = 0;      // this warp's tiles of the run: positions t0 + 32 W j, j in [j0, j1)
+    int idb = 0, ids = -1, ids_next = -1;  // lane 2 k + s: index (in 16 rows) of half s of tile idb + k; -1 none, -2 bad
+    int run_hi = 0, run_h = 0;
+    const int32_t* table = nullptr;
+    auto rows16 = [&](int j) {
+        const int t = t0 + kAttnUnit * W * (j + (lane >> 1)) + kAttnSub * (lane & 1);
+        if (t >= run_hi || j + (lane >> 1) >= j1) return -1;
+        const int col = t / a.page, page = table[col];
+        return page < 0 || page >= a.pages ? -2 : int((int64_t(page) * a.kv_heads + run_h) * (a.page / kAttnSub)) + (t - col * a.page) / kAttnSub;
+    };
+    auto begin = [&](const Run* r) {
+        attn_warp_units(r->t0, r->n, w, W, r->lo, r->hi, &j0, &j1);
+        t0 = r->t0 + kAttnUnit * w;
+        run_hi = r->hi;
+        run_h = r->h;
+        table = a.table + int64_t(r->b) * a.table_stride;
+        idb = j0;
+        ids = rows16(j0);
+        ids_next = rows16(j0 + 16);
+    };
+    uint32_t live = 0;  // two bits a ring slot: its halves were copied
+    auto issue = [&](int j, int slot) {
+        if (j < j1) {
+            if (j - idb == 16) {
+                idb = j;
+                ids = ids_next;
+                ids_next = rows16(j + 16);
+            }
+            const int r0 = __shfl_sync(kFull, ids, 2 * (j - idb)), r1 = __shfl_sync(kFull, ids, 2 * (j - idb) + 1);
+            bad |= r0 == -2 || r1 == -2;
+            live = (live & ~(3u << (2 * slot))) | ((r0 >= 0 ? 1u : 0u) | (r1 >= 0 ? 2u : 0u)) << (2 * slot);
+            // halves that are not there copy the pool's first rows, and are masked
+            const int64_t at0 = r0 < 0 ? 0 : r0, at1 = r1 < 0 ? 0 : r1;
+            const uint32_t off = slot * F::TILE;
+            const uint8_t* const k0 = ksrc + at0 * (kAttnSub * D / 2);
+            const uint8_t* const k1 = ksrc + at1 * (kAttnSub * D / 2);
+            const uint8_t* const v0 = vsrc + at0 * (kAttnSub * D / 2);
+            const uint8_t* const v1 = vsrc + at1 * (kAttnSub * D / 2);
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                cp_async_16(cdst[i] + off, k0 + i * 512);
+                cp_async_16(cdst[i] + off + F::CODES / 2, k1 + i * 512);
+                cp_async_16(cdst[i] + off + F::CODES, v0 + i * 512);
+                cp_async_16(cdst[i] + off + F::CODES + F::CODES / 2, v1 + i * 512);
+            }
+            const int64_t sat = (s_sub ? at1 : at0) * (kAttnSub * NG * 2);
+#pragma unroll
+            for (int i = 0; i < SPT; ++i) {
+                const uint32_t dst = ring + off + 2 * F::CODES + (i * 32 + lane) * 16;
+                if constexpr (16 * NG >= 32) cp_async_16(dst, ssrc[i] + sat);
+                else if (s_on) cp_async_16(dst, ssrc[i] + sat);
+            }
         }
-        Run r;
-        const int64_t in = x - before;
-        const int item = int(in / s.units);
-        r.u0 = int(in - int64_t(item) * s.units);
-        r.n = int(x_end - x < s.units - r.u0 ? x_end - x : s.units - r.u0);
-        r.b = b;
-        r.h = item / s.rt;
-        r.rt = item - r.h * s.rt;
-        r.row_lo = r.rt * R;
-        const int nrows = s.n * a.group_heads;
-        r.rows = nrows - r.row_lo < R ? nrows - r.row_lo : R;
-        attn_range(s, r.row_lo, r.row_lo + r.rows, a.group_heads, a.window, a.tree != nullptr, &r.lo, &r.hi);
-        {
-            const int first = s.start + r.row_lo / a.group_heads;
-            const int last = s.start + (r.row_lo + r.rows - 1) / a.group_heads;
-            r.full_hi = a.tree ? s.start : first + 1;
-            if (r.full_hi > s.keys) r.full_hi = s.keys;
-            r.full_lo = a.window > 0 && last >= a.window ? last - a.window + 1 : 0;
-        }
-        if (s.start + s.n > a.capacity) bad = true;  // the table cannot name all of its positions
-        const bool whole = r.n == s.units;
+        sm100::cp_async_commit();
+    };
 
+    // eight values of Q, for thread-item i of a run's rows
+    auto load_q = [&](const Run* r, int i) {
+        const int row = i / (D / 8), p8 = i % (D / 8);
+        if (row >= r->rows) return make_uint4(0u, 0u, 0u, 0u);
+        const int qr = r->row_lo + row, tok = qr / a.group_heads, hg = qr - tok * a.group_heads;
+        const uint16_t* src = a.q + int64_t(r->row0 + tok) * a.q_ts + int64_t(r->h * a.group_heads + hg) * a.q_hs + p8 * 8;
+        if (a.q_vec) return *reinterpret_cast<const uint4*>(src);
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = uint32_t(src[2 * j]) | uint32_t(src[2 * j + 1]) << 16;
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    };
+    uint4 q_first = load_q(cur, tid);  // on its way while the tiles' pages are looked up
+    begin(cur);
+#pragma unroll
+    for (int i = 0; i < F::RING - F::MS; ++i) issue(j0 + i, F::MS + i);
+    while (true) {
         // ---- Q: fragments in shared memory, scaled by a power of two per row
-        for (int i = tid; i < R * (D / 8); i += 32 * kAttnWarps) {
+        for (int i = tid; i < R * (D / 8); i += THREADS) {
             const int row = i / (D / 8), p8 = i % (D / 8);  // eight values from 8 * p8
             float v[8];
-            const int qr = r.row_lo + row, tok = qr / a.group_heads, hg = qr - tok * a.group_heads;
-            if (row < r.rows) {
-                const uint16_t* src = a.q + int64_t(s.row0 + tok) * a.q_ts + int64_t(r.h * a.group_heads + hg) * a.q_hs + p8 * 8;
-                uint32_t raw[4];
-                if (a.q_vec) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(src);
-                    raw[0] = u.x, raw[1] = u.y, raw[2] = u.z, raw[3] = u.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) raw[j] = uint32_t(src[2 * j]) | uint32_t(src[2 * j + 1]) << 16;
-                }
+            {
+                const uint4 u = i == tid ? q_first : load_q(cur, i);
+                const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[2 * j] = a.is_bf16 ? bf16lo_to_f32(raw[j]) : half_lo(raw[j]);
                     v[2 * j + 1] = a.is_bf16 ? bf16hi_to_f32(raw[j]) : half_hi(raw[j]);
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.f;
             }
+            const int tok = (cur->row_lo + row) / a.group_heads;
             float mx = 0.f, sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[j])), sum += v[j];
+            for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[j]));
 #pragma unroll
             for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-#pragma unroll
-            for (int o = 1; o < GRP / 8; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
             // exponent e with max * 2^e in [2^14, 2^15); rows of zeros, infinities or NaN: 0
             int e = 0;
             if (mx > 0.f && mx < INFINITY) e = 14 + 127 - int(__float_as_uint(mx) >> 23);
             if (e > 126) e = 126;  // subnormal rows
             const float up = exp2i(e);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= up;
+            for (int j = 0; j < 8; ++j) v[j] *= up, sum += v[j];
+#pragma unroll
+            for (int o = 1; o < GRP / 8; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
             // nibbles 0, 2 of a pair's place are codes * 2^-24, nibbles 1, 3 codes * 2^-20
             uint4 f;
             f.x = f32x2_to_f16x2(v[0], v[4]);
@@ -297,87 +413,48 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
             f.w = f32x2_to_f16x2(v[3] * 0.0625f, v[7] * 0.0625f);
             const int nt = row >> 3, ch = p8 >> 2, ln = (row & 7) * 4 + (p8 & 3);
             sts_v4(sbase + F::OFF_Q + ((nt * CH + ch) * 32 + ln) * 16, f);
-            if (p8 % (GRP / 8) == 0)
-                *reinterpret_cast<float*>(smem + F::OFF_QB + (row * NG + p8 / (GRP / 8)) * 4) = sum * a.scale_log2;
+            if (p8 % (GRP / 8) == 0) {
+                // the group's sum in the same units, as three fp16 terms
+                const float s0 = sum * 0x1p-24f, h0 = __half2float(__float2half_rn(s0));
+                const float s1 = s0 - h0, h1 = __half2float(__float2half_rn(s1));
+                uint32_t* qb = reinterpret_cast<uint32_t*>(smem + F::OFF_QB + (row * NG + p8 / (GRP / 8)) * 8);
+                qb[0] = f32x2_to_f16x2(h0, h1);
+                qb[1] = f32x2_to_f16x2(s1 - h1, 0.f);
+            }
             if (p8 == 0) {
                 // 2^24 * 2^-e in two exact steps (e may be as low as -113)
                 *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * 16777216.f * exp2i(-e);
-                *reinterpret_cast<int*>(smem + F::OFF_LIM + row * 4) = row < r.rows ? s.start + tok : INT_MAX;
+                *reinterpret_cast<int*>(smem + F::OFF_LIM + row * 4) = row < cur->rows ? cur->start + tok : INT_MAX;
                 *reinterpret_cast<int64_t*>(smem + F::OFF_BITS + row * 8) =
-                    a.tree != nullptr && row < r.rows ? a.tree[s.row0 + tok] : -1;
+                    a.tree != nullptr && row < cur->rows ? a.tree[cur->row0 + tok] : -1;
             }
         }
         __syncthreads();
+        // the slots that the last item's sums were in
+#pragma unroll
+        for (int i = F::RING - F::MS; i < F::RING - 1; ++i) issue(j0 + i, (F::MS + i) % F::RING);
 
-        float qf[NT][2], qb[NT][2][NG];
+        // constants of the queries: in registers for one column of them, else from shared memory each time
+        constexpr int QBM = (NG + 3) / 4;  // MMAs for the biases: four groups each
+        auto q_frag = [&](int nt, int ch) { return lds_v4(sbase + F::OFF_Q + ((nt * CH + ch) * 32 + lane) * 16); };
+        auto q_factor = [&](int nt) { return lds_f2(sbase + F::OFF_F + (nt * 8 + 2 * c) * 4); };
+        auto q_bias = [&](int nt, int m) {
+            const uint2 v = lds_u2(sbase + F::OFF_QB + ((nt * 8 + g) * NG + m * 4 + (NG < 4 ? c % NG : c)) * 8);
+            return m * 4 + c < NG ? v : make_uint2(0u, 0u);
+        };
         uint4 qreg[NT == 1 ? CH : 1];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int row = nt * 8 + 2 * c + k;
-                qf[nt][k] = *reinterpret_cast<const float*>(smem + F::OFF_F + row * 4);
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    qb[nt][k][j] = *reinterpret_cast<const float*>(smem + F::OFF_QB + (row * NG + j) * 4);
-            }
+        float2 qfreg = make_float2(0.f, 0.f);
+        uint2 qbreg[NT == 1 ? QBM : 1];
         if constexpr (NT == 1) {
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) qreg[ch] = lds_v4(sbase + F::OFF_Q + (ch * 32 + lane) * 16);
+            for (int ch = 0; ch < CH; ++ch) qreg[ch] = q_frag(0, ch);
+            qfreg = q_factor(0);
+#pragma unroll
+            for (int m = 0; m < QBM; ++m) qbreg[m] = q_bias(0, m);
         }
 
-        // ---- this warp's tiles: positions t0 + 64 j, j in [j0, j1)
-        const int t0 = s.lo + kAttnUnit * r.u0 + kAttnTile * w;
-        int j0 = r.lo > t0 + kAttnTile - 1 ? (r.lo - (t0 + kAttnTile - 1) + kAttnUnit - 1) / kAttnUnit : 0;
-        int j1 = r.hi > t0 ? (r.hi - t0 + kAttnUnit - 1) / kAttnUnit : 0;
-        if (j1 > r.n) j1 = r.n;
-        const int32_t* table = a.table + int64_t(b) * a.table_stride;
-        auto page_of = [&](int j) { return j < j1 ? table[(t0 + kAttnUnit * j) / a.page] : -1; };
-        int idb = j0, ids = page_of(j0 + lane), ids_next = page_of(j0 + 32 + lane);
-        uint32_t live = 0;  // bit per ring slot: the tile there was copied
-
-        auto issue = [&](int j, int slot) {
-            if (j < j1) {
-                if (j - idb == 32) {
-                    idb = j;
-                    ids = ids_next;
-                    ids_next = page_of(j + 32 + lane);
-                }
-                const int page = __shfl_sync(kFull, ids, j - idb);
-                if (page >= 0 && page < a.pages) {
-                    live |= 1u << slot;
-                    const int t = t0 + kAttnUnit * j;
-                    const int64_t row = (int64_t(page) * a.kv_heads + r.h) * a.page + t % a.page;
-                    const uint32_t dst = ring + slot * F::TILE;
-                    const uint8_t* ksrc = a.kc + row * (D / 2) + lane * 16;
-                    const uint8_t* vsrc = a.vc + row * (D / 2) + lane * 16;
-#pragma unroll
-                    for (int i = 0; i < CPT; ++i) {
-                        const int piece = i * 32 + lane;
-                        const uint32_t o = swz(piece / CH, piece % CH);
-                        cp_async_16(dst + o, ksrc + i * 512);
-                        cp_async_16(dst + F::CODES + o, vsrc + i * 512);
-                    }
-#pragma unroll
-                    for (int i = 0; i < SPT; ++i) {
-                        const int piece = i * 32 + lane;
-                        if (8 * NG % 32 == 0 || piece < 8 * NG) {
-                            const int arr = piece / (2 * NG), at = piece % (2 * NG);
-                            const uint8_t* base = reinterpret_cast<const uint8_t*>(
-                                arr == 0 ? a.ks : arr == 1 ? a.kb : arr == 2 ? a.vs : a.vb);
-                            cp_async_16(dst + 2 * F::CODES + piece * 16, base + row * (NG * 2) + at * 16);
-                        }
-                    }
-                } else {
-                    live &= ~(1u << slot);
-                    bad = true;
-                }
-            }
-            sm100::cp_async_commit();
-        };
-
         // sums, relative to the queries' references
-        float ref[NT][2], l[NT][2], bs[NT][2][NG], o[NT][CH][2][4];
+        float ref[NT][2], l[NT][2], bs[NT][2][NG], o[NT][CH][2][4], os[F::SUMS ? NT : 1][F::SUMS ? NG : 1][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -392,144 +469,174 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[nt][ch][m][i] = 0.f;
+            if constexpr (F::SUMS) {
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) os[nt][j][i] = 0.f;
+            }
         }
 
-        auto tile = [&](int t, uint32_t st, auto masked_c) {
+        // SUBS halves of a tile from its half h0 on; `there`: bit per half of the tile that was copied
+        auto part = [&](int t, uint32_t st, int h0, uint32_t there, auto masked_c) {
             constexpr bool MASKED = decltype(masked_c)::value;
+            const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: this lane's row and piece
+            const int kch = lane >> 4;
             // which of this lane's (position, query) pairs are seen
-            uint32_t see = 0xFFFFFFFFu;
-            bool in0 = true, in1 = true;
-            if constexpr (MASKED) {
-                in0 = t + g < s.keys, in1 = t + g + 8 < s.keys;
-                see = 0;
+            uint32_t see[SUBS];
+            bool in[SUBS][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < SUBS; ++u) {
+                see[u] = 0xFFFFFFFFu;
+                in[u][0] = in[u][1] = true;
+                if constexpr (MASKED) {
+                    see[u] = 0;
+                    const bool ok = (there >> (h0 + u)) & 1;
+                    const int tu = t + kAttnSub * (h0 + u) + g;
+                    in[u][0] = ok && tu < cur->keys, in[u][1] = ok && tu + 8 < cur->keys;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = nt * 8 + 2 * c + (i & 1), p = t + g + (i >> 1) * 8;
-                        bool ok;
-                        if (a.tree != nullptr) {
-                            const int64_t bits = *reinterpret_cast<const int64_t*>(smem + F::OFF_BITS + row * 8);
-                            const int d = p - s.start;
-                            ok = d < 0 || (d < 64 && ((bits >> d) & 1));
-                        } else {
-                            const int lim = *reinterpret_cast<const int*>(smem + F::OFF_LIM + row * 4);
-                            ok = p <= lim && (a.window <= 0 || lim == INT_MAX || p > lim - a.window);
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = nt * 8 + 2 * c + (i & 1), p = tu + (i >> 1) * 8;
+                            bool on;
+                            if (a.tree != nullptr) {
+                                const int64_t bits = *reinterpret_cast<const int64_t*>(smem + F::OFF_BITS + row * 8);
+                                const int d = p - cur->start;
+                                on = d < 0 || (d < 64 && ((bits >> d) & 1));
+                            } else {
+                                const int lim = *reinterpret_cast<const int*>(smem + F::OFF_LIM + row * 4);
+                                on = p <= lim && (a.window <= 0 || lim == INT_MAX || p > lim - a.window);
+                            }
+                            if (on && in[u][i >> 1]) see[u] |= 1u << (nt * 4 + i);
                         }
-                        if (ok && p < s.keys) see |= 1u << (nt * 4 + i);
-                    }
+                }
             }
-            // ---- scores: code sums per group, scaled
-            float acc[NT][4];
-            float bias[NT][4];
-            {
-                float ks0[NG], ks1[NG], kb0[NG], kb1[NG];
-                const uint32_t sb = st + 2 * F::CODES + g * (2 * NG);
-                lds_halves<NG>(sb, ks0);
-                lds_halves<NG>(sb + 16 * NG, ks1);
-                lds_halves<NG>(sb + F::SB, kb0);
-                lds_halves<NG>(sb + F::SB + 16 * NG, kb1);
+            // ---- scores.  acc = sum over groups of b * sum(Q) (one MMA) + s * code sums
+            float acc[SUBS][NT][4], ks[SUBS][2][NG];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < SUBS; ++u) {
+                const uint32_t sb = st + 2 * F::CODES + (kAttnSub * (h0 + u) + g) * (2 * NG);
+                lds_halves<NG>(sb, ks[u][0]);
+                lds_halves<NG>(sb + 16 * NG, ks[u][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        bias[nt][i] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < NG; ++j)
-                            bias[nt][i] = fmaf(i < 2 ? kb0[j] : kb1[j], qb[nt][i & 1][j], bias[nt][i]);
-                        acc[nt][i] = 0.f;
-                    }
-                float part[NT][4];
-                uint32_t kw[4];
-                const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch) {
-                    if (ch % 2 == 0) ldsm_x4(st + swz(krow, ch + (lane >> 4)), kw);
-                    const uint32_t w0 = kw[2 * (ch & 1)], w1 = kw[2 * (ch & 1) + 1];
-                    const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
-                    const uint32_t e0 = w0 & 0x000F000Fu, e1 = w1 & 0x000F000Fu, e2 = h0 & 0x000F000Fu, e3 = h1 & 0x000F000Fu;
-                    const uint32_t f0 = w0 & 0x00F000F0u, f1 = w1 & 0x00F000F0u, f2 = h0 & 0x00F000F0u, f3 = h1 & 0x00F000F0u;
+                for (int m = 0; m < QBM; ++m) {
+                    const uint32_t at = sb + F::SB + (m * 4 + (NG < 4 ? c % NG : c)) * 2;
+                    uint16_t b0, b1;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b0) : "r"(at));
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b1) : "r"(at + 16 * NG));
+                    const uint32_t p0 = b0 * 0x10001u, p1 = b1 * 0x10001u;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 q = NT == 1 ? qreg[NT == 1 ? ch : 0] : lds_v4(sbase + F::OFF_Q + ((nt * CH + ch) * 32 + lane) * 16);
-                        if (ch * 32 % GRP == 0) mma_16816_z(part[nt], e0, e1, e2, e3, q.x, q.y);
-                        else mma_16816(part[nt], e0, e1, e2, e3, q.x, q.y);
-                        mma_16816(part[nt], f0, f1, f2, f3, q.z, q.w);
+                        const uint2 qb = NT == 1 ? qbreg[NT == 1 ? m : 0] : q_bias(nt, m);
+                        if (m == 0) mma_16816_z(acc[u][nt], p0, p1, p0, p1, qb.x, qb.y);
+                        else mma_16816(acc[u][nt], p0, p1, p0, p1, qb.x, qb.y);
                     }
-                    if ((ch + 1) * 32 % GRP == 0) {
-                        const int j = ch * 32 / GRP;
+                }
+            }
+            {
+                float sums[SUBS][NT][4];
+                uint32_t kw[SUBS][4];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[nt][i] = fmaf(i < 2 ? ks0[j] : ks1[j], part[nt][i], acc[nt][i]);
+                    for (int u = 0; u < SUBS; ++u) {
+                        if (ch % 2 == 0) ldsm_x4(st + swz(kAttnSub * (h0 + u) + krow, ch + kch), kw[u]);
+                        const uint32_t w0 = kw[u][2 * (ch & 1)], w1 = kw[u][2 * (ch & 1) + 1];
+                        const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
+                        const uint32_t e0 = w0 & 0x000F000Fu, e1 = w1 & 0x000F000Fu, e2 = y0 & 0x000F000Fu, e3 = y1 & 0x000F000Fu;
+                        const uint32_t f0 = w0 & 0x00F000F0u, f1 = w1 & 0x00F000F0u, f2 = y0 & 0x00F000F0u, f3 = y1 & 0x00F000F0u;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 q = NT == 1 ? qreg[NT == 1 ? ch : 0] : q_frag(nt, ch);
+                            if (ch * 32 % GRP == 0) mma_16816_z(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
+                            else mma_16816(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
+                            mma_16816(sums[u][nt], f0, f1, f2, f3, q.z, q.w);
+                        }
+                        if ((ch + 1) * 32 % GRP == 0) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    acc[u][nt][i] = fmaf(ks[u][i >> 1][ch * 32 / GRP], sums[u][nt][i], acc[u][nt][i]);
+                        }
                     }
                 }
             }
             // ---- probabilities, V's scales applied, packed for the second product
-            float vs0[NG], vs1[NG], vb0[NG], vb1[NG];
-            {
-                const uint32_t sb = st + 2 * F::CODES + 2 * F::SB + g * (2 * NG);
-                lds_halves<NG>(sb, vs0);
-                lds_halves<NG>(sb + 16 * NG, vs1);
-                lds_halves<NG>(sb + F::SB, vb0);
-                lds_halves<NG>(sb + F::SB + 16 * NG, vb1);
+            float vs[SUBS][2][NG], vb[SUBS][2][NG];
 #pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    if constexpr (MASKED) {
-                        if (!in0) vs0[j] = vb0[j] = 0.f;
-                        if (!in1) vs1[j] = vb1[j] = 0.f;
+            for (int u = 0; u < SUBS; ++u) {
+                const uint32_t sb = st + 2 * F::CODES + 2 * F::SB + (kAttnSub * (h0 + u) + g) * (2 * NG);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    lds_halves<NG>(sb + k * 16 * NG, vs[u][k]);
+                    lds_halves<NG>(sb + F::SB + k * 16 * NG, vb[u][k]);
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+                        if (MASKED && !in[u][k]) vs[u][k][j] = vb[u][k][j] = 0.f;
+                        vb[u][k][j] = fmaf(8.f, vs[u][k][j], vb[u][k][j]);
                     }
-                    vb0[j] = fmaf(8.f, vs0[j], vb0[j]);
-                    vb1[j] = fmaf(8.f, vs1[j], vb1[j]);
                 }
             }
-            float p[NT][4];
-            uint32_t pk[NT][NG][2];
+            float p[SUBS][NT][4];
+            uint32_t pk[SUBS][NT][NG][2];
             auto probabilities = [&]() -> bool {
                 uint32_t any = 0;
                 float top = -INFINITY;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int u = 0; u < SUBS; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float xv = fmaf(qf[nt][i & 1], acc[nt][i], bias[nt][i] - ref[nt][i & 1]);
-                        if (MASKED && !((see >> (nt * 4 + i)) & 1)) xv = -INFINITY;
-                        top = fmaxf(top, xv);
-                        p[nt][i] = ex2(xv);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 qf = NT == 1 ? qfreg : q_factor(nt);
 #pragma unroll
-                    for (int j = 0; j < NG; ++j) {
-                        float m0 = p[nt][0] * vs0[j], m1 = p[nt][1] * vs0[j], m2 = p[nt][2] * vs1[j], m3 = p[nt][3] * vs1[j];
-                        if constexpr (MASKED) {
-                            if (!((see >> (nt * 4)) & 1)) m0 = 0.f;
-                            if (!((see >> (nt * 4 + 1)) & 1)) m1 = 0.f;
-                            if (!((see >> (nt * 4 + 2)) & 1)) m2 = 0.f;
-                            if (!((see >> (nt * 4 + 3)) & 1)) m3 = 0.f;
+                        for (int i = 0; i < 4; ++i) {
+                            float xv = fmaf(i & 1 ? qf.y : qf.x, acc[u][nt][i], -ref[nt][i & 1]);
+                            if (MASKED && !((see[u] >> (nt * 4 + i)) & 1)) xv = -INFINITY;
+                            top = fmaxf(top, xv);
+                            p[u][nt][i] = ex2(xv);
                         }
-                        pk[nt][j][0] = f32x2_to_f16x2(m0, m1);
-                        pk[nt][j][1] = f32x2_to_f16x2(m2, m3);
-                        any |= pk[nt][j][0] | pk[nt][j][1];
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) {
+                            float m[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                m[i] = p[u][nt][i] * vs[u][i >> 1][j];
+                                if (MASKED && !((see[u] >> (nt * 4 + i)) & 1)) m[i] = 0.f;
+                            }
+                            pk[u][nt][j][0] = f32x2_to_f16x2(m[0], m[1]);
+                            pk[u][nt][j][1] = f32x2_to_f16x2(m[2], m[3]);
+                            any |= pk[u][nt][j][0] | pk[u][nt][j][1];
+                        }
                     }
-                }
                 return (any & 0x40004000u) != 0 || top > 60.f;
             };
             if (__any_sync(kFull, probabilities())) {
-                // new references from this tile: the largest P * s becomes 2^-4 (and P at most 2^20)
-                float sg0 = 0.f, sg1 = 0.f;
+                // new references from these positions: the largest P * s becomes 2^-4 (and P at most 2^20)
+                float lg[SUBS][2];
 #pragma unroll
-                for (int j = 0; j < NG; ++j) sg0 = fmaxf(sg0, fabsf(vs0[j])), sg1 = fmaxf(sg1, fabsf(vs1[j]));
-                const float l0 = lg2(sg0), l1 = lg2(sg1);
+                for (int u = 0; u < SUBS; ++u)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int k = 0; k < 2; ++k) {
+                        float m = 0.f;
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) m = fmaxf(m, fabsf(vs[u][k][j]));
+                        lg[u][k] = lg2(m) + 4.f;
+                    }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 qf = NT == 1 ? qfreg : q_factor(nt);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float m = -INFINITY;
 #pragma unroll
-                        for (int i = k; i < 4; i += 2) {
-                            const float sc = fmaf(qf[nt][k], acc[nt][i], bias[nt][i]);
-                            const float v = fmaxf(sc + (i < 2 ? l0 : l1) + 4.f, sc - 20.f);
-                            if (!MASKED || ((see >> (nt * 4 + i)) & 1)) m = fmaxf(m, v);
-                        }
+                        for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+                            for (int i = k; i < 4; i += 2) {
+                                const float sc = (k ? qf.y : qf.x) * acc[u][nt][i];
+                                const float v = fmaxf(sc + lg[u][i >> 1], sc - 20.f);
+                                if (!MASKED || ((see[u] >> (nt * 4 + i)) & 1)) m = fmaxf(m, v);
+                            }
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
                         const float nr = fmaxf(ref[nt][k], m);
@@ -542,69 +649,90 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
                         for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
                             for (int mm = 0; mm < 2; ++mm) o[nt][ch][mm][k] *= f, o[nt][ch][mm][k + 2] *= f;
+                        if constexpr (F::SUMS) {
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) os[nt][j][k] *= f, os[nt][j][k + 2] *= f;
+                        }
                     }
+                }
                 probabilities();
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                l[nt][0] += p[nt][0] + p[nt][2];
-                l[nt][1] += p[nt][1] + p[nt][3];
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    if constexpr (MASKED) {
-                        bs[nt][0][j] += ((see >> (nt * 4)) & 1) ? p[nt][0] * vb0[j] : 0.f;
-                        bs[nt][1][j] += ((see >> (nt * 4 + 1)) & 1) ? p[nt][1] * vb0[j] : 0.f;
-                        bs[nt][0][j] += ((see >> (nt * 4 + 2)) & 1) ? p[nt][2] * vb1[j] : 0.f;
-                        bs[nt][1][j] += ((see >> (nt * 4 + 3)) & 1) ? p[nt][3] * vb1[j] : 0.f;
-                    } else {
-                        bs[nt][0][j] = fmaf(p[nt][2], vb1[j], fmaf(p[nt][0], vb0[j], bs[nt][0][j]));
-                        bs[nt][1][j] = fmaf(p[nt][3], vb1[j], fmaf(p[nt][1], vb0[j], bs[nt][1][j]));
-                    }
-                    pk[nt][j][0] = movmatrix_trans(pk[nt][j][0]);
-                    pk[nt][j][1] = movmatrix_trans(pk[nt][j][1]);
-                }
-            }
-            // ---- sums over V: rows d = 32 ch + 4 g + {m, m + 2}
-            uint32_t vw[4];
-            const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                if (ch % 2 == 0) ldsm_x4_trans(st + F::CODES + swz(vrow, ch + (lane >> 4)), vw);
-                const uint32_t w0 = vw[2 * (ch & 1)], w1 = vw[2 * (ch & 1) + 1];
-                const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
-                constexpr uint32_t m8 = 0x80088008u, m80 = 0x80808080u;  // -8 * 2^-24, -8 * 2^-20
-                const uint32_t e0 = hadd2_bits(w0 & 0x000F000Fu, m8), e1 = hadd2_bits(h0 & 0x000F000Fu, m8);
-                const uint32_t e2 = hadd2_bits(w1 & 0x000F000Fu, m8), e3 = hadd2_bits(h1 & 0x000F000Fu, m8);
-                const uint32_t f0 = hadd2_bits(w0 & 0x00F000F0u, m80), f1 = hadd2_bits(h0 & 0x00F000F0u, m80);
-                const uint32_t f2 = hadd2_bits(w1 & 0x00F000F0u, m80), f3 = hadd2_bits(h1 & 0x00F000F0u, m80);
-                const int j = ch * 32 / GRP;
+            for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816(o[nt][ch][0], e0, e1, e2, e3, pk[nt][j][0], pk[nt][j][1]);
-                    mma_16816(o[nt][ch][1], f0, f1, f2, f3, pk[nt][j][0], pk[nt][j][1]);
+                    l[nt][0] += p[u][nt][0] + p[u][nt][2];
+                    l[nt][1] += p[u][nt][1] + p[u][nt][3];
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (MASKED) bs[nt][i & 1][j] += ((see[u] >> (nt * 4 + i)) & 1) ? p[u][nt][i] * vb[u][i >> 1][j] : 0.f;
+                            else bs[nt][i & 1][j] = fmaf(p[u][nt][i], vb[u][i >> 1][j], bs[nt][i & 1][j]);
+                        }
+                        pk[u][nt][j][0] = movmatrix_trans(pk[u][nt][j][0]);
+                        pk[u][nt][j][1] = movmatrix_trans(pk[u][nt][j][1]);
+                        if constexpr (F::SUMS)  // 8 * 2^-24 in every row: the sum of P * s, for the centre of the codes
+                            mma_16816(os[nt][j], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pk[u][nt][j][0], pk[u][nt][j][1]);
+                    }
+                }
+            // ---- sums over V: rows d = 32 ch + 4 g + {m, m + 2}
+            uint32_t vw[SUBS][4];
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                const int j = ch * 32 / GRP;
+#pragma unroll
+                for (int u = 0; u < SUBS; ++u) {
+                    if (ch % 2 == 0) ldsm_x4_trans(st + F::CODES + swz(kAttnSub * (h0 + u) + krow, ch + kch), vw[u]);
+                    const uint32_t w0 = vw[u][2 * (ch & 1)], w1 = vw[u][2 * (ch & 1) + 1];
+                    const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
+                    uint32_t e0 = w0 & 0x000F000Fu, e1 = y0 & 0x000F000Fu, e2 = w1 & 0x000F000Fu, e3 = y1 & 0x000F000Fu;
+                    uint32_t f0 = w0 & 0x00F000F0u, f1 = y0 & 0x00F000F0u, f2 = w1 & 0x00F000F0u, f3 = y1 & 0x00F000F0u;
+                    if constexpr (!F::SUMS) {
+                        constexpr uint32_t m8 = 0x80088008u, m80 = 0x80808080u;  // -8 * 2^-24, -8 * 2^-20
+                        e0 = hadd2_bits(e0, m8), e1 = hadd2_bits(e1, m8), e2 = hadd2_bits(e2, m8), e3 = hadd2_bits(e3, m8);
+                        f0 = hadd2_bits(f0, m80), f1 = hadd2_bits(f1, m80), f2 = hadd2_bits(f2, m80), f3 = hadd2_bits(f3, m80);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(o[nt][ch][0], e0, e1, e2, e3, pk[u][nt][j][0], pk[u][nt][j][1]);
+                        mma_16816(o[nt][ch][1], f0, f1, f2, f3, pk[u][nt][j][0], pk[u][nt][j][1]);
+                    }
                 }
             }
         };
 
         // ---- stream the tiles
-#pragma unroll
-        for (int i = 0; i < F::RING - 1; ++i) issue(j0 + i, i);
-        int slot = 0;
+        int slot = F::MS % F::RING;
+        const int full_lo = cur->full_lo, full_hi = cur->full_hi;
         for (int j = j0; j < j1; ++j) {
             sm100::cp_async_wait<F::RING - 2>();
             __syncwarp();
             issue(j + F::RING - 1, slot == 0 ? F::RING - 1 : slot - 1);
-            const int t = t0 + kAttnUnit * j;
-            if ((live >> slot) & 1) {
-                if (t >= r.full_lo && t + kAttnTile <= r.full_hi) tile(t, ring + slot * F::TILE, std::false_type{});
-                else tile(t, ring + slot * F::TILE, std::true_type{});
+            const int t = t0 + kAttnUnit * W * j;
+            const uint32_t there = (live >> (2 * slot)) & 3u, st = ring + slot * F::TILE;
+            if (there == 3 && t >= full_lo && t + kAttnUnit <= full_hi) {
+#pragma unroll
+                for (int h0 = 0; h0 < 2; h0 += SUBS) part(t, st, h0, there, std::false_type{});
+            } else if (there) {
+#pragma unroll 1
+                for (int h0 = 0; h0 < 2; h0 += SUBS) part(t, st, h0, there, std::true_type{});
             }
             slot = slot == F::RING - 1 ? 0 : slot + 1;
         }
         sm100::cp_async_wait<0>();
         __syncwarp();
 
-        // ---- the warp's sums to shared memory (its own, drained ring)
+        // ---- the next item's first tiles are fetched while this one's sums are put together
+        const int x = pl.pieces ? x_end : cur->x + cur->n;
+        const bool more = x < x_end;
+        if (more) {
+            bad |= plan(next, x, cur->b, cur->before, false);
+            q_first = load_q(next, tid);
+            begin(next);
+#pragma unroll
+            for (int i = 0; i < F::RING - F::MS; ++i) issue(j0 + i, F::MS + i);
+        }
         float* mo = reinterpret_cast<float*>(smem + w * F::WARP);
         float* ml = mo + R * F::OROW;
 #pragma unroll
@@ -621,7 +749,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
                 if (g == 0) ml[row] = ref[nt][k], ml[R + row] = l[nt][k];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    const float bb = bs[nt][k][ch * 32 / GRP];
+                    float bb = bs[nt][k][ch * 32 / GRP];
+                    if constexpr (F::SUMS) bb = fmaf(os[nt][ch * 32 / GRP][k], -16777216.f, bb);
                     float4 v;
                     v.x = fmaf(o[nt][ch][0][k], 16777216.f, bb);
                     v.y = fmaf(o[nt][ch][1][k], 1048576.f, bb);
@@ -632,19 +761,24 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
             }
         __syncthreads();
         // ---- the block's sums: to the output, or to this block's slot of the workspace
-        float* slot_o = a.part + int64_t(attn_slot(blockIdx.x, first_item)) * F::SLOT;
-        for (int i = tid; i < r.rows * (D / 4); i += 32 * kAttnWarps) {
+        const bool whole = cur->n == cur->units;
+        auto put = [&](int row, int d, float4 sum, float lsum, float top) {
+            const int qr = cur->row_lo + row, tok = qr / a.group_heads;
+            store_row4(a, cur->row0 + tok, cur->h * a.group_heads + qr - tok * a.group_heads, d, sum, lsum, top);
+        };
+        float* slot_o = a.part + int64_t(attn_slot(blockIdx.x, cur->first)) * F::SLOT;
+        for (int i = tid; i < cur->rows * (D / 4); i += THREADS) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
-            float rf[kAttnWarps], top = kNoRef;
+            float rf[W], top = kNoRef;
 #pragma unroll
-            for (int k = 0; k < kAttnWarps; ++k) {
+            for (int k = 0; k < W; ++k) {
                 rf[k] = reinterpret_cast<const float*>(smem + k * F::WARP)[R * F::OROW + row];
                 top = fmaxf(top, rf[k]);
             }
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             float lsum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kAttnWarps; ++k) {
+            for (int k = 0; k < W; ++k) {
                 const float* from = reinterpret_cast<const float*>(smem + k * F::WARP);
                 const float f = ex2(rf[k] - top);
                 const float4 v = *reinterpret_cast<const float4*>(from + row * F::OROW + d);
@@ -653,116 +787,82 @@ __global__ void __launch_bounds__(32 * kAttnWarps, NT == 1 && D <= 128 ? 4 : D =
                 lsum = fmaf(f, from[R * F::OROW + R + row], lsum);
             }
             if (whole) {
-                const int qr = r.row_lo + row, tok = qr / a.group_heads;
-                const int head = r.h * a.group_heads + qr - tok * a.group_heads;
-                store_row4(a, s.row0 + tok, head, d, sum, lsum, top);
+                put(row, d, sum, lsum, top);
             } else {
-                *reinterpret_cast<float4*>(slot_o + row * D + d) = sum;
-                if (d == 0) slot_o[R * D + row] = top, slot_o[R * D + R + row] = lsum;
+                __stcg(reinterpret_cast<float4*>(slot_o + row * D + d), sum);
+                if (d == 0) __stcg(slot_o + R * D + row, top), __stcg(slot_o + R * D + R + row, lsum);
             }
         }
-        __syncthreads();
-        x += r.n;
-        first_item = false;
-    }
-    if (bad && lane == 0) atomicOr(&g_attn_errors, 2u);
-}
-
-// Sums the items that several blocks shared: one block a (item, row), its warps over the
-// partial sums in block order.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks) {
-    constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4 a lane (lanes past D / 4 idle at D = 64)
-    constexpr int SLOT = ROWS * (D + 2);
-    __shared__ float4 so[8][D / 4];
-    __shared__ float sl[8];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const int64_t total = all_units(a, ROWS, lane);
-    int64_t before;
-    // block = (item, row): the sequence from the rows in front of it
-    const int64_t at = blockIdx.x;
-    const int b = find_seq(a.seqs, at, lane, &before, [&](int i) { return int64_t(load_seq(a, i, ROWS).rt) * a.kv_heads * ROWS; });
-    if (b >= a.seqs) return;
-    const AttnSeq s = load_seq(a, b, ROWS);
-    const int item = int((at - before) / ROWS), row = int((at - before) % ROWS);
-    const int h = item / s.rt, rt = item - h * s.rt;
-    const int qr = rt * ROWS + row;
-    if (qr >= s.n * a.group_heads) return;
-    int64_t units_before;
-    // units in front of the sequence: the same search, by units
-    {
-        int64_t sum = 0;
-        for (int i = lane; i < b; i += 32) sum += attn_seq_units(load_seq(a, i, ROWS), a.kv_heads);
-        units_before = warp_sum64(sum);
-    }
-    const int64_t x0 = units_before + int64_t(item) * s.units;
-    const int64_t shares = attn_shares(total, blocks);
-    const int c0 = attn_owner(x0, total, shares), c1 = attn_owner(x0 + s.units - 1, total, shares);
-    if (c0 == c1) return;  // written by its block
-    // the first block's share may begin before the item
-    auto slot_of = [&](int i) {
-        return a.part + int64_t(attn_slot(i, attn_share(i, total, shares) >= x0)) * SLOT;
-    };
-    float top = kNoRef;
-    for (int i = c0 + lane; i <= c1; i += 32) top = fmaxf(top, slot_of(i)[ROWS * D + row]);
+        if (!whole) {
+            // the last of the item's blocks to arrive adds their sums in block order
+            const int c0 = cur->c0, c1 = cur->c1;
+            __threadfence();
+            __syncthreads();
+            int* flag = reinterpret_cast<int*>(smem + F::OFF_LAST);
+            if (tid == 0) *flag = atomicInc(a.count + c0, unsigned(c1 - c0)) == unsigned(c1 - c0);  // wraps to 0
+            __syncthreads();
+            if (*flag) {
+                __threadfence();
+                // the item is the first of its blocks, but for c0 where that began in front of it
+                const bool c0_first = pl.pieces || c0 * pl.per == cur->x - cur->u0;
+                auto slot_of = [&](int i) { return a.part + int64_t(attn_slot(i, i > c0 || c0_first)) * F::SLOT; };
+                for (int i = tid; i < cur->rows * (D / 4); i += THREADS) {
+                    const int row = i / (D / 4), d = i % (D / 4) * 4;
+                    float top = kNoRef, lsum = 0.f;
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int q0 = c0; q0 <= c1; q0 += 8) {
+                        float4 v[8];
+                        float rf[8], ll[8], nt = top;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    float4 sum[V];
-    float lsum = 0.f;
+                        for (int k = 0; k < 8; ++k) {
+                            const bool on = q0 + k <= c1;
+                            const float* from = slot_of(on ? q0 + k : c1);
+                            rf[k] = on ? __ldcg(from + R * D + row) : kNoRef;
+                            ll[k] = on ? __ldcg(from + R * D + R + row) : 0.f;
+                            v[k] = on ? __ldcg(reinterpret_cast<const float4*>(from + row * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
 #pragma unroll
-    for (int k = 0; k < V; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = c0 + w; i <= c1; i += 8) {
-        const float* from = slot_of(i);
-        const float f = ex2(from[ROWS * D + row] - top);
-        lsum = fmaf(f, from[ROWS * D + ROWS + row], lsum);
+                        for (int k = 0; k < 8; ++k) nt = fmaxf(nt, rf[k]);
+                        const float f0 = ex2(top - nt);
+                        sum.x *= f0, sum.y *= f0, sum.z *= f0, sum.w *= f0, lsum *= f0;
+                        top = nt;
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            if (k * 32 + lane < D / 4) {
-                const float4 v = *reinterpret_cast<const float4*>(from + row * D + (k * 32 + lane) * 4);
-                sum[k].x = fmaf(f, v.x, sum[k].x), sum[k].y = fmaf(f, v.y, sum[k].y);
-                sum[k].z = fmaf(f, v.z, sum[k].z), sum[k].w = fmaf(f, v.w, sum[k].w);
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = ex2(rf[k] - top);
+                            sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
+                            sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
+                            lsum = fmaf(f, ll[k], lsum);
+                        }
+                    }
+                    put(row, d, sum, lsum, top);
+                }
             }
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-        if (k * 32 + lane < D / 4) so[w][k * 32 + lane] = sum[k];
-    if (lane == 0) sl[w] = lsum;
-    __syncthreads();
-    if (threadIdx.x < D / 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float ls = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v.x += so[k][threadIdx.x].x, v.y += so[k][threadIdx.x].y;
-            v.z += so[k][threadIdx.x].z, v.w += so[k][threadIdx.x].w;
-            ls += sl[k];
         }
-        const int tok = qr / a.group_heads, head = h * a.group_heads + qr - tok * a.group_heads;
-        store_row4(a, s.row0 + tok, head, threadIdx.x * 4, v, ls, top);
+        if (!more) break;
+        __syncthreads();  // the sums' ring slots and Q are free
+        Run* const was = cur;
+        cur = next;
+        next = was;
     }
+    if (__any_sync(kFull, bad) && lane == 0) atomicOr(&g_attn_errors, 2u);
 }
 
 using AttnFn = void (*)(const AttnArgs);
-using JoinFn = void (*)(const AttnArgs, int);
 struct AttnInst {
     AttnFn fn;
-    JoinFn join;
-    int smem, slot, rows;
+    int smem, slot, rows, threads;
 };
 
 template <int D, int GRP, int NT>
 AttnInst inst() {
     using F = AttnFmt<D, GRP, NT>;
-    static_assert(F::SMEM <= 227 * 1024, "larger than a block's shared memory");
-    return AttnInst{attn_kernel<D, GRP, NT>, attn_join_kernel<D, F::ROWS>, F::SMEM, F::SLOT, F::ROWS};
+    static_assert(F::SMEM <= 114 * 1024, "two blocks do not fit an SM");
+    return AttnInst{attn_kernel<D, GRP, NT>, F::SMEM, F::SLOT, F::ROWS, 32 * F::W};
 }
 template <int D, int GRP>
 AttnInst inst_nt(int nt) {
     if constexpr (D == 256) return nt == 1 ? inst<D, GRP, 1>() : inst<D, GRP, 2>();
-    else return nt == 1 ? inst<D, GRP, 1>() : nt == 2 ? inst<D, GRP, 2>() : inst<D, GRP, 4>();
+    else return nt == 1 ? inst<D, GRP, 1>() : nt == 2 ? inst<D, GRP, 2>() : nt == 3 ? inst<D, GRP, 3>() : inst<D, GRP, 4>();
 }
 AttnInst instance(int d, int grp, int nt) {
     if (d == 64) return grp == 32 ? inst_nt<64, 32>(nt) : inst_nt<64, 64>(nt);
@@ -787,7 +887,7 @@ cudaError_t attn_resident(const AttnInst& k, int* out) {
     e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e != cudaSuccess) return e;
     int per = 0, sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k.fn, 32 * kAttnWarps, size_t(k.smem));
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k.fn, k.threads, size_t(k.smem));
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -801,11 +901,13 @@ cudaError_t attn_resident(const AttnInst& k, int* out) {
 
 cudaError_t launch_attn(const AttnArgs& in, int head_dim, int group, cudaStream_t stream) {
     AttnArgs a = in;
-    // query rows of a tile: as many 8-row columns as the average sequence has rows for, so that the
-    // cache is streamed once wherever the rows fit
-    const int64_t rows = (int64_t(a.tokens) + a.seqs - 1) / a.seqs * a.group_heads;
-    const int nt = rows <= 8 ? 1 : rows <= 16 || head_dim == 256 ? 2 : 4;
-    const AttnInst k = instance(head_dim, group, nt);
+    // query rows of a tile: the 8-row columns that the sequences' rows fill, so that the cache is
+    // streamed once wherever they fit.  Only the average is known here; where it is not a whole
+    // number the counts differ, and the longest are taken to have half as many tokens again
+    const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
+    const int64_t rows = (a.tokens % a.seqs ? mean + mean / 2 : mean) * a.group_heads;
+    const int64_t cols = (rows + 7) / 8, most = head_dim == 256 ? 2 : 4;
+    const AttnInst k = instance(head_dim, group, int(cols < most ? cols : most));
     int blocks = 0;
     cudaError_t e = attn_resident(k, &blocks);
     if (e != cudaSuccess) return e;
@@ -813,11 +915,15 @@ cudaError_t launch_attn(const AttnArgs& in, int head_dim, int group, cudaStream_
     const int64_t tiles = int64_t(a.tokens) * a.group_heads / k.rows + a.seqs;
     const int64_t per_item = (int64_t(a.capacity) + kAttnUnit - 1) / kAttnUnit;
     const int64_t units = tiles * a.kv_heads * (per_item > 0 ? per_item : 1);
+    if (units >= int64_t(1) << 30) return cudaErrorNotSupported;
     if (units < blocks) blocks = int(units);
+    if (blocks > kArrivalCounters) blocks = kArrivalCounters;
     void* ws = nullptr;
     e = split_workspace(stream, size_t(2) * blocks * k.slot * sizeof(float), &ws);
     if (e != cudaSuccess) return e;
     a.part = static_cast<float*>(ws);
+    e = arrival_counters(stream, &a.count);
+    if (e != cudaSuccess) return e;
 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -827,14 +933,9 @@ cudaError_t launch_attn(const AttnArgs& in, int head_dim, int group, cudaStream_
     cfg.numAttrs = 1;
     cfg.stream = stream;
     cfg.gridDim = dim3(unsigned(blocks));
-    cfg.blockDim = dim3(32 * kAttnWarps);
+    cfg.blockDim = dim3(unsigned(k.threads));
     cfg.dynamicSmemBytes = size_t(k.smem);
-    e = cudaLaunchKernelEx(&cfg, k.fn, static_cast<const AttnArgs>(a));
-    if (e != cudaSuccess || blocks == 1 || per_item <= 1) return e;  // nothing can be shared
-    cfg.gridDim = dim3(unsigned(tiles * a.kv_heads * k.rows));
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, k.join, static_cast<const AttnArgs>(a), blocks);
+    return cudaLaunchKernelEx(&cfg, k.fn, static_cast<const AttnArgs>(a));
 }
 
 cudaError_t attn_read_and_clear_errors(unsigned* out) {

@@ -92,6 +92,10 @@ bool stream_supported(int64_t M, int64_t N, int64_t K, int bits, int group);
 // and kept: the partial sums and arrival words of tiles that several blocks share.  Calls on
 // one stream run in order and may share it.
 cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out);
+// Arrival counters of a stream (and of each graph capture in progress on it), zero between calls:
+// whoever counts with them leaves them zero (atomicInc that wraps at the last arrival does).
+constexpr int kArrivalCounters = 4096;
+cudaError_t arrival_counters(cudaStream_t stream, unsigned** out);
 // A fresh 48-bit tag for the arrival words of one call (never 0).
 unsigned long long next_call_token();
 
@@ -172,7 +176,8 @@ struct AttnArgs {
     const int32_t *table, *lens, *cu;
     const int64_t* tree;                   // [tokens] or null
     int64_t table_stride;
-    float* part;                           // partial sums (set by the launch)
+    float* part;                           // partial sums and arrival counters (set by the launch)
+    unsigned* count;
     int64_t pages;
     int page, capacity;                    // positions a page, and that a table row can name
     int seqs, tokens, kv_heads, group_heads, window;

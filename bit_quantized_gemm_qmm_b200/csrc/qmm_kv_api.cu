@@ -29,6 +29,8 @@ qmm_status check_cache(const qmm_kv_cache* c) {
         return fail(QMM_ERR_UNSUPPORTED, "kv_heads=%d (1..%d)", c->kv_heads, kMaxHeads);
     if (c->pages < 1 || c->pages > INT32_MAX)
         return fail(QMM_ERR_INVALID_ARG, "pages=%lld", (long long)c->pages);
+    if (c->pages * c->kv_heads > (int64_t(1) << 31) / (c->page_size / 16) - 1)
+        return fail(QMM_ERR_UNSUPPORTED, "pages * kv_heads * page_size: more than 2^35 rows");
     const void* p[6] = {c->k_packed, c->k_scales, c->k_biases, c->v_packed, c->v_scales, c->v_biases};
     for (const void* q : p)
         if (!q || !aligned(q, 16)) return fail(QMM_ERR_INVALID_ARG, "the cache's arrays must be 16-byte aligned pointers");

@@ -13,9 +13,8 @@
 
 namespace qmm_impl {
 
-constexpr int kAttnTile = 16;                        // positions a warp takes at a time
-constexpr int kAttnWarps = 4;                        // warps a block
-constexpr int kAttnUnit = kAttnTile * kAttnWarps;    // positions a block takes at a time
+constexpr int kAttnSub = 16;              // positions whose page is looked up once (pages are multiples of it)
+constexpr int kAttnUnit = 2 * kAttnSub;   // positions a warp takes at a time: attention's unit of work
 
 // One sequence of an attention call.
 struct AttnSeq {
@@ -23,9 +22,10 @@ struct AttnSeq {
     int n;       // its new tokens (query rows)
     int start;   // cache position of the first of them (negative where the length is too short)
     int keys;    // positions that exist: its length, at most what its page table can name
-    int lo;      // first position that a query sees, rounded down to a tile
+    int lo;      // first position that a query sees, rounded down to a multiple of kAttnSub
     int units;   // units of positions [lo, keys) (one at least, so that empty rows are written)
     int rt;      // tiles of `rows` query rows (new tokens x heads of a K/V head)
+    bool falls;  // its offsets fall: the sums over sequences have no bound then, and nothing is done
 };
 
 QMM_HD int clamp_int(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
@@ -36,6 +36,7 @@ QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int g
     AttnSeq s;
     s.row0 = clamp_int(c0, 0, tokens);
     s.n = clamp_int(c1, 0, tokens) - s.row0;
+    s.falls = c1 < c0;
     if (s.n < 0) s.n = 0;
     if (len < 0) len = 0;
     s.start = len - s.n;
@@ -44,7 +45,7 @@ QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int g
     if (window > 0 && s.start >= window) {  // the first query sees positions from start - window + 1
         s.lo = s.start - window + 1;
         if (s.lo > s.keys) s.lo = s.keys;
-        s.lo -= s.lo % kAttnTile;
+        s.lo -= s.lo % kAttnSub;
     }
     s.units = (s.keys - s.lo + kAttnUnit - 1) / kAttnUnit;
     if (s.units < 1) s.units = 1;
@@ -53,15 +54,59 @@ QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int g
 }
 
 // All units of a sequence: items (K/V head, row tile), row tiles next to one another, each of
-// s.units units of positions.
-QMM_HD int64_t attn_seq_units(const AttnSeq& s, int kv_heads) { return int64_t(kv_heads) * s.rt * s.units; }
+// s.units units of positions.  The host bounds the sum over all sequences (of offsets
+// that do not fall) below 2^30.
+QMM_HD int attn_seq_items(const AttnSeq& s, int kv_heads) { return kv_heads * s.rt; }
+QMM_HD int attn_seq_units(const AttnSeq& s, int kv_heads) { return attn_seq_items(s, kv_heads) * s.units; }
 
-// Blocks take even, contiguous shares of all units, none of them empty: of `shares` blocks, block i
-// takes [attn_share(i), attn_share(i + 1)).
-QMM_HD int64_t attn_shares(int64_t total, int64_t blocks) { return total < blocks ? total : blocks; }
-QMM_HD int64_t attn_share(int64_t i, int64_t total, int64_t shares) { return i * total / shares; }
-// The block that takes unit x.
-QMM_HD int attn_owner(int64_t x, int64_t total, int64_t shares) { return int(((x + 1) * shares - 1) / total); }
+QMM_HD int ceil_div_int(int a, int b) { return (a - 1) / b + 1; }  // a >= 1
+
+// How the work is dealt out over `blocks` blocks.  Few items: each is cut into pieces of `per` units (the
+// last one shorter), one a block, so that no block has to change items; the pieces are as small as
+// keeps their number within the blocks, and give each of a block's warps a unit at least.  Many items:
+// block i takes units [i * per, (i + 1) * per) of all, across items.
+struct AttnPlan {
+    int total, per, pieces;  // units of all; units a block; 1: pieces
+};
+QMM_HD AttnPlan attn_plan(int total, int items, int blocks, int warps) {
+    AttnPlan p;
+    p.total = total;
+    p.pieces = items <= blocks / 2;
+    p.per = total < 1 ? 1 : ceil_div_int(total, p.pieces ? blocks - items : blocks);
+    if (p.pieces && p.per < warps) p.per = warps;
+    return p;
+}
+
+// Weight of a sequence in the order of the blocks: what find_seq adds up.
+QMM_HD int attn_seq_weight(const AttnPlan& p, const AttnSeq& s, int kv_heads) {
+    return p.pieces ? attn_seq_items(s, kv_heads) * ceil_div_int(s.units, p.per) : attn_seq_units(s, kv_heads);
+}
+
+// A block's share of an item.  x: the place in the order of the blocks (the block itself, or a unit),
+// `before` the weight of the sequences in front.
+struct AttnShare {
+    int item, u0, n;  // item of the sequence, first unit, units
+    int c0, c1;       // the blocks that share the item
+};
+QMM_HD AttnShare attn_share(const AttnPlan& p, const AttnSeq& s, int x, int x_end, int before) {
+    AttnShare h;
+    const int in = x - before;
+    if (p.pieces) {
+        const int np = ceil_div_int(s.units, p.per);
+        h.item = in / np;
+        h.u0 = (in - h.item * np) * p.per;
+        h.n = s.units - h.u0 < p.per ? s.units - h.u0 : p.per;
+        h.c0 = before + h.item * np;
+        h.c1 = h.c0 + np - 1;
+    } else {
+        h.item = in / s.units;
+        h.u0 = in - h.item * s.units;
+        h.n = s.units - h.u0 < x_end - x ? s.units - h.u0 : x_end - x;
+        h.c0 = (x - h.u0) / p.per;
+        h.c1 = (x - h.u0 + s.units - 1) / p.per;
+    }
+    return h;
+}
 
 // Positions [lo, hi) that rows [r0, r1) (row = token * group_heads + head) of a sequence can see.
 QMM_HD void attn_range(const AttnSeq& s, int r0, int r1, int group_heads, int window, bool tree, int* lo, int* hi) {
@@ -70,9 +115,19 @@ QMM_HD void attn_range(const AttnSeq& s, int r0, int r1, int group_heads, int wi
     *lo = window > 0 && first >= window ? first - window + 1 : 0;
 }
 
-// A block writes the partial sums of an item it does not take whole to one of two slots: the
-// first item of its share to slot 2i, its last to 2i + 1 (there are no others: those between
-// are whole).
+// Of n units from position t0 of an item (t0 = its lo + kAttnUnit * first unit), a block's warp w takes
+// units w, w + warps, ...: those numbered [j0, j1) of them hold positions in [lo, hi).
+QMM_HD void attn_warp_units(int t0, int n, int w, int warps, int lo, int hi, int* j0, int* j1) {
+    const int t = t0 + kAttnUnit * w, step = kAttnUnit * warps;
+    *j0 = lo > t + kAttnUnit - 1 ? (lo - (t + kAttnUnit - 1) + step - 1) / step : 0;
+    int last = hi > t ? (hi - t + step - 1) / step : 0;
+    const int mine = n > w ? (n - w + warps - 1) / warps : 0;
+    *j1 = last < mine ? last : mine;
+}
+
+// A block writes the sums of an item it does not take whole to one of two slots: those of the first
+// item of its share to slot 2 i, of its last to 2 i + 1 (those between are whole).  An item is the
+// first of each of its blocks but perhaps c0.
 QMM_HD int attn_slot(int block, bool first_item) { return 2 * block + (first_item ? 0 : 1); }
 
 }  // namespace qmm_impl

@@ -1169,6 +1169,41 @@ cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out) {
     return cudaSuccess;
 }
 
+cudaError_t arrival_counters(cudaStream_t stream, unsigned** out) {
+    static std::unordered_map<WsKey, unsigned*, WsKeyHash> all;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    unsigned long long cid = 0;
+    e = cudaStreamGetCaptureInfo(stream, &st, &cid);
+    if (e != cudaSuccess) return e;
+    const WsKey key{dev, reinterpret_cast<uintptr_t>(stream), st == cudaStreamCaptureStatusActive ? cid : 0ull};
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    auto it = all.find(key);
+    if (it != all.end()) {
+        *out = it->second;
+        return cudaSuccess;
+    }
+    // as in split_workspace; the zeros are written by a stream of its own, once
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    void* ptr = nullptr;
+    cudaStream_t own = nullptr;
+    e = cudaMalloc(&ptr, kArrivalCounters * sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, kArrivalCounters * sizeof(unsigned), own);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+    if (own) cudaStreamDestroy(own);
+    if (e != cudaSuccess && ptr) cudaFree(ptr);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    *out = static_cast<unsigned*>(ptr);
+    all.emplace(key, *out);
+    return cudaSuccess;
+}
+
 // Call tags start at a value taken from the clock, so that arrival words left in reused
 // device memory by another process (whose tags started elsewhere) do not match this one's.
 unsigned long long next_call_token() {

@@ -282,7 +282,8 @@ qmm_status qmm_batched(const void* x, int64_t x_stride, const uint32_t* packed, 
  * like) are [cu_tokens[b], cu_tokens[b + 1]).  Page tables, lengths and offsets are read on the
  * device, in stream order, so that a captured graph may be replayed with other contents.  Rows of
  * the token axis in front of cu_tokens[0] or from cu_tokens[seqs] on belong to no sequence and
- * are left as they are; offsets are clamped to [0, tokens].
+ * are left as they are; offsets are clamped to [0, tokens].  Offsets must not fall (attention
+ * then does nothing and sets bit 1 of qmm_device_errors()).
  *
  * What only the device can see is checked there: a position beyond max_pages * page_size, a
  * negative one, or a page outside [0, pages) is not accessed (append, copy and compact skip it,
@@ -295,7 +296,7 @@ typedef struct {
     uint32_t* v_packed;  /* V's, likewise.  All six 16-byte aligned, owned by the caller     */
     uint16_t* v_scales;
     uint16_t* v_biases;
-    int64_t pages;
+    int64_t pages;       /* pages * kv_heads * page_size below 2^35                          */
     int32_t page_size;   /* a multiple of 16 up to 1024                                      */
     int32_t kv_heads;    /* 1..256                                                           */
     int32_t head_dim;    /* 64, 128 or 256                                                   */
@@ -372,7 +373,9 @@ qmm_status qmm_kv_compact(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, co
  * in it, NaN included.  Arithmetic: codes enter the tensor cores exactly; scores, softmax and sums
  * are fp32; each probability times V's scale is rounded once to fp16, q to fp16 relative to its
  * row's largest value (exact unless 2^-24 below it), o once.  Results do not depend on timing.
- * Uses the stream's workspace (as qmm).
+ * Uses the stream's workspace (as qmm), a captured call one of its capture: two instances of one
+ * captured graph must not run at once.  The tiles of 8 query rows or more that the new tokens make,
+ * times kv_heads, times max_pages * page_size / 32, must stay below 2^30.
  */
 qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const void* q, int64_t q_token_stride,
                             int64_t q_head_stride, void* o, int64_t o_token_stride,

@@ -255,9 +255,16 @@ def test_attention_bad_pages_and_lengths():
     o, lse = q.kv_attention(c, x, table[:, :1], longer, cu)
     torch.cuda.synchronize()
     assert q.device_errors() == 2 and lse[0].isnan().all()
-    # offsets that fall or leave the rows
-    for off in ([0, 5, 2, 3, 4, 5, 6, 7, 8], [-7, 1, 2, 3, 4, 5, 6, 7, 10 ** 6], [8] * 9, [0] * 9):
+    # offsets that leave the rows, and that fall (nothing is done)
+    for off in ([-7, 1, 2, 3, 4, 5, 6, 7, 10 ** 6], [8] * 9, [0] * 9):
         q.kv_attention(c, x, table, lens, ints(off))
+    torch.cuda.synchronize()
+    q.device_errors()
+    out = torch.full_like(x, 7.0)
+    for off in ([0, 5, 2, 3, 4, 5, 6, 7, 8], [2 ** 31 - 1, -2 ** 31] * 4 + [0]):
+        q.kv_attention(c, x, table, lens, ints(off), out=out)
+        torch.cuda.synchronize()
+        assert q.device_errors() == 2 and (out == 7).all()
     q.kv_attention(c, x, table, ints([-5, -2 ** 31, 0, 1, 2, 3, 4, 5]), cu)
     torch.cuda.synchronize()
     q.device_errors()
