@@ -42,16 +42,18 @@ def _stale(srcs, target) -> bool:
 
 
 def build_call_module(force: bool = False) -> str:
-    """gcc the CPython hand-off module (plain C against the interpreter's headers)."""
+    """gcc the CPython hand-off module (plain C against the interpreter's headers and torch's dlpack.h)."""
     deps = (CALL_SRC, os.path.join(HERE, "..", "include", "qmm.h"), __file__)
     if not force and os.path.exists(CALL_LIB) and os.path.getmtime(CALL_LIB) >= max(map(os.path.getmtime, deps)):
         return CALL_LIB
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if not cc:
         raise RuntimeError("no C compiler for the _qmm_call module")
+    import torch  # for the place of its headers
+    torch_include = os.path.join(os.path.dirname(torch.__file__), "include")
     tmp = CALL_LIB + ".tmp"
     subprocess.check_call([cc, "-O2", "-shared", "-fPIC", "-Wall", "-Werror",
-                           "-I" + sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp])
+                           "-I" + sysconfig.get_paths()["include"], "-I" + torch_include, CALL_SRC, "-o", tmp])
     os.replace(tmp, CALL_LIB)
     return CALL_LIB
 

@@ -12,6 +12,8 @@
 #include <Python.h>
 #include <stdint.h>
 
+#include <ATen/dlpack.h> /* torch's copy of the exchange format: plain C */
+
 #include "../include/qmm.h"
 
 typedef int (*qmm_ex_fn)(const void* x, const uint32_t* packed, const uint16_t* scales,
@@ -60,7 +62,9 @@ static PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     return PyLong_FromLong(st);
 }
 
-/* ---- the K/V cache: five functions of the ABI, bound together ---- */
+/* ---- the K/V cache: five functions of the ABI, bound together.  They take tensors, read through
+ * torch's DLPack exchange functions (a view of a tensor's pointer, sizes and strides in about the
+ * time of one attribute look-up), and check what the ABI cannot see. ---- */
 static struct {
     qmm_status (*append)(const qmm_kv_cache*, const void*, int64_t, int64_t, const void*, int64_t, int64_t,
                          const qmm_kv_seqs*, const int32_t*, int64_t, qmm_dtype, void*);
@@ -72,36 +76,132 @@ static struct {
                             const qmm_kv_seqs*, const int32_t*, int64_t, int, float, int64_t, const int64_t*,
                             qmm_dtype, void*);
 } g_kv;
+static const DLPackExchangeAPI* g_dl = NULL;
+static PyTypeObject* g_tensor = NULL;
 
-/* The first n arguments as 64-bit integers (addresses too); 0 and an exception if one is none. */
-static int ints(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want, Py_ssize_t n, int64_t* v) {
+/* A call's cache: the address of its descriptor and its device. */
+typedef struct {
+    const qmm_kv_cache* cache;
+    int device;
+    void* stream;
+} ctx;
+
+static int is_type(const DLTensor* t, int code, int bits) {
+    return t->dtype.code == code && t->dtype.bits == bits && t->dtype.lanes == 1;
+}
+
+/* View of a tensor of `dims` dimensions on the call's device; 0 and an exception if it is none. */
+static int view(const ctx* x, PyObject* obj, const char* what, int dims, DLTensor* t) {
+    if (!PyObject_TypeCheck(obj, g_tensor)) {
+        PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
+        return 0;
+    }
+    if (g_dl->dltensor_from_py_object_no_sync(obj, t) != 0) {
+        if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%s cannot be read", what);
+        return 0;
+    }
+    if (t->device.device_type != kDLCUDA || t->device.device_id != x->device || t->ndim != dims) {
+        PyErr_Format(PyExc_ValueError, "%s must be a tensor of %d dimension%s on the cache's CUDA device", what, dims,
+                     dims == 1 ? "" : "s");
+        return 0;
+    }
+    return 1;
+}
+static void* data(const DLTensor* t) { return (char*)t->data + t->byte_offset; }
+
+/* A contiguous vector of n values (n < 0: any number) of a type. */
+static int vec(const ctx* x, PyObject* obj, const char* what, int64_t n, int code, int bits, DLTensor* t) {
+    if (!view(x, obj, what, 1, t)) return 0;
+    if (!is_type(t, code, bits) || (n >= 0 && t->shape[0] != n) || (t->shape[0] > 1 && t->strides && t->strides[0] != 1)) {
+        PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s%d vector of %s%lld values", what,
+                     code == kDLInt ? "int" : "float", bits, n < 0 ? "any number, not " : "", (long long)(n < 0 ? t->shape[0] : n));
+        return 0;
+    }
+    return 1;
+}
+
+/* [tokens, heads, head_dim] rows with a contiguous last dimension. */
+typedef struct {
+    void* p;
+    int64_t ts, hs, tokens, heads;
+    int dtype;
+} rows;
+static int rows_of(const ctx* x, PyObject* obj, const char* what, rows* r) {
+    DLTensor t;
+    if (!view(x, obj, what, 3, &t)) return 0;
+    r->dtype = is_type(&t, kDLFloat, 16) ? QMM_F16 : is_type(&t, kDLBfloat, 16) ? QMM_BF16 : -1;
+    if (r->dtype < 0) {
+        PyErr_Format(PyExc_ValueError, "%s must be fp16 or bf16", what);
+        return 0;
+    }
+    r->tokens = t.shape[0], r->heads = t.shape[1];
+    const int64_t dim = t.shape[2];
+    const int64_t s0 = t.strides ? t.strides[0] : t.shape[1] * dim, s1 = t.strides ? t.strides[1] : dim;
+    if (dim != x->cache->head_dim || (t.strides && t.strides[2] != 1)) {
+        PyErr_Format(PyExc_ValueError, "%s must have contiguous rows of head_dim=%d values", what, (int)x->cache->head_dim);
+        return 0;
+    }
+    r->p = data(&t), r->ts = r->tokens > 1 ? s0 : 0, r->hs = r->heads > 1 ? s1 : 0;
+    return 1;
+}
+
+/* The cache's descriptor address and device, and the device's current stream. */
+static int begin(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want, ctx* x) {
     if (nargs != want) {
         PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", want, nargs);
         return 0;
     }
-    if (g_kv.append == NULL) {
+    if (g_dl == NULL) {
         PyErr_SetString(PyExc_RuntimeError, "the K/V cache functions are not bound");
         return 0;
     }
-    for (Py_ssize_t i = 0; i < n; ++i) {
-        v[i] = (int64_t)PyLong_AsLongLong(args[i]);
-        if (v[i] == -1 && PyErr_Occurred()) return 0;
+    x->cache = (const qmm_kv_cache*)PyLong_AsVoidPtr(args[0]);
+    x->device = (int)PyLong_AsLong(args[1]);
+    x->stream = NULL;
+    if (PyErr_Occurred()) return 0;
+    if (x->cache == NULL) {
+        PyErr_SetString(PyExc_ValueError, "the cache's address is null");
+        return 0;
     }
     return 1;
 }
-#define PTR(type, x) ((type)(uintptr_t)(x))
-/* table, its row stride, columns, sequences, offsets */
-static qmm_kv_seqs seqs_of(const int64_t* v) {
-    qmm_kv_seqs s = {PTR(const int32_t*, v[0]), PTR(const int32_t*, v[4]), v[3], v[1], v[2]};
-    return s;
+static int stream_of(ctx* x) {
+    if (g_dl->current_work_stream(kDLCUDA, x->device, &x->stream) == 0) return 1;
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "no current stream");
+    return 0;
 }
 
-/* bind_kv(append, gather, copy_pages, compact, attention): the functions' addresses */
+/* Page table, offsets and one value a sequence (`at`). */
+static int seqs_of(const ctx* x, PyObject* table, PyObject* at, const char* at_name, PyObject* cu, const char* cu_name,
+                   qmm_kv_seqs* s, const int32_t** at_out) {
+    DLTensor t, c, v;
+    if (!view(x, table, "page_table", 2, &t)) return 0;
+    if (!is_type(&t, kDLInt, 32) || (t.shape[1] > 1 && t.strides && t.strides[1] != 1)) {
+        PyErr_SetString(PyExc_ValueError, "page_table must be int32 [seqs, pages] with contiguous rows");
+        return 0;
+    }
+    if (!vec(x, at, at_name, t.shape[0], kDLInt, 32, &v) || !vec(x, cu, cu_name, t.shape[0] + 1, kDLInt, 32, &c)) return 0;
+    s->page_table = (const int32_t*)data(&t);
+    s->cu_tokens = (const int32_t*)data(&c);
+    s->seqs = t.shape[0];
+    s->max_pages = t.shape[1];
+    s->table_stride = t.shape[0] > 1 && t.strides ? t.strides[0] : t.shape[1];
+    *at_out = (const int32_t*)data(&v);
+    return 1;
+}
+
+static int same_rows(const rows* a, const rows* b, const char* what) {
+    if (a->tokens == b->tokens && a->heads == b->heads && a->dtype == b->dtype) return 1;
+    PyErr_SetString(PyExc_ValueError, what);
+    return 0;
+}
+
+/* bind_kv(append, gather, copy_pages, compact, attention, tensor type): the functions' addresses */
 static PyObject* bind_kv(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
     void* p[5];
-    if (nargs != 5) {
-        PyErr_SetString(PyExc_TypeError, "bind_kv takes 5 addresses");
+    if (nargs != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind_kv takes 5 addresses and the tensor type");
         return NULL;
     }
     for (int i = 0; i < 5; ++i) {
@@ -111,72 +211,120 @@ static PyObject* bind_kv(PyObject* self, PyObject* const* args, Py_ssize_t nargs
             return NULL;
         }
     }
+    if (!PyType_Check(args[5])) {
+        PyErr_SetString(PyExc_TypeError, "the tensor type expected");
+        return NULL;
+    }
+    PyObject* capsule = PyObject_GetAttrString(args[5], "__dlpack_c_exchange_api__");
+    if (capsule == NULL) return NULL;
+    const DLPackExchangeAPI* api = (const DLPackExchangeAPI*)PyCapsule_GetPointer(capsule, "dlpack_exchange_api");
+    Py_DECREF(capsule); /* the functions live as long as the process */
+    if (api == NULL) return NULL;
+    if (api->header.version.major != DLPACK_MAJOR_VERSION || api->dltensor_from_py_object_no_sync == NULL ||
+        api->current_work_stream == NULL) {
+        PyErr_SetString(PyExc_RuntimeError, "this torch's DLPack exchange functions are of another version");
+        return NULL;
+    }
     *(void**)&g_kv.append = p[0];
     *(void**)&g_kv.gather = p[1];
     *(void**)&g_kv.copy_pages = p[2];
     *(void**)&g_kv.compact = p[3];
     *(void**)&g_kv.attention = p[4];
+    Py_INCREF(args[5]);
+    Py_XDECREF((PyObject*)g_tensor);
+    g_tensor = (PyTypeObject*)args[5];
+    g_dl = api;
     Py_RETURN_NONE;
 }
 
-/* cache, k, strides (token, head), v, strides, seqs (5), lens, tokens, dtype, stream */
+/* cache, device, k, v, page_table, lens, cu_tokens */
 static PyObject* kv_append(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
-    int64_t v[16];
-    if (!ints(args, nargs, 16, 16, v)) return NULL;
-    const qmm_kv_seqs s = seqs_of(v + 7);
-    return PyLong_FromLong(g_kv.append(PTR(const qmm_kv_cache*, v[0]), PTR(void*, v[1]), v[2], v[3], PTR(void*, v[4]), v[5],
-                                       v[6], &s, PTR(const int32_t*, v[12]), v[13], (qmm_dtype)v[14], PTR(void*, v[15])));
+    ctx x;
+    rows k, v;
+    qmm_kv_seqs s;
+    const int32_t* lens;
+    if (!begin(args, nargs, 7, &x) || !rows_of(&x, args[2], "k", &k) || !rows_of(&x, args[3], "v", &v)) return NULL;
+    if (!same_rows(&k, &v, "k and v must have one shape and dtype")) return NULL;
+    if (k.heads != x.cache->kv_heads) {
+        PyErr_Format(PyExc_ValueError, "k and v must have kv_heads=%d heads", (int)x.cache->kv_heads);
+        return NULL;
+    }
+    if (!seqs_of(&x, args[4], args[5], "lens", args[6], "cu_tokens", &s, &lens) || !stream_of(&x)) return NULL;
+    return PyLong_FromLong(g_kv.append(x.cache, k.p, k.ts, k.hs, v.p, v.ts, v.hs, &s, lens, k.tokens, (qmm_dtype)k.dtype, x.stream));
 }
 
-/* cache, seqs (5), starts, tokens, k, strides, v, strides, dtype, stream */
+/* cache, device, k, v, page_table, starts, cu_tokens */
 static PyObject* kv_gather(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
-    int64_t v[16];
-    if (!ints(args, nargs, 16, 16, v)) return NULL;
-    const qmm_kv_seqs s = seqs_of(v + 1);
-    return PyLong_FromLong(g_kv.gather(PTR(const qmm_kv_cache*, v[0]), &s, PTR(const int32_t*, v[6]), v[7], PTR(void*, v[8]),
-                                       v[9], v[10], PTR(void*, v[11]), v[12], v[13], (qmm_dtype)v[14], PTR(void*, v[15])));
+    ctx x;
+    rows k, v;
+    qmm_kv_seqs s;
+    const int32_t* starts;
+    if (!begin(args, nargs, 7, &x) || !rows_of(&x, args[2], "out[0]", &k) || !rows_of(&x, args[3], "out[1]", &v)) return NULL;
+    if (!same_rows(&k, &v, "the outputs must have one shape and dtype")) return NULL;
+    if (k.heads != x.cache->kv_heads) {
+        PyErr_Format(PyExc_ValueError, "the outputs must have kv_heads=%d heads", (int)x.cache->kv_heads);
+        return NULL;
+    }
+    if (!seqs_of(&x, args[4], args[5], "starts", args[6], "cu_tokens", &s, &starts) || !stream_of(&x)) return NULL;
+    return PyLong_FromLong(g_kv.gather(x.cache, &s, starts, k.tokens, k.p, k.ts, k.hs, v.p, v.ts, v.hs, (qmm_dtype)k.dtype, x.stream));
 }
 
-/* cache, src, dst, pairs, stream */
+/* cache, device, src, dst */
 static PyObject* kv_copy_pages(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
-    int64_t v[5];
-    if (!ints(args, nargs, 5, 5, v)) return NULL;
-    return PyLong_FromLong(g_kv.copy_pages(PTR(const qmm_kv_cache*, v[0]), PTR(const int32_t*, v[1]),
-                                           PTR(const int32_t*, v[2]), v[3], PTR(void*, v[4])));
+    ctx x;
+    DLTensor a, b;
+    if (!begin(args, nargs, 4, &x) || !vec(&x, args[2], "src", -1, kDLInt, 32, &a) ||
+        !vec(&x, args[3], "dst", a.shape[0], kDLInt, 32, &b) || !stream_of(&x))
+        return NULL;
+    return PyLong_FromLong(g_kv.copy_pages(x.cache, (const int32_t*)data(&a), (const int32_t*)data(&b), a.shape[0], x.stream));
 }
 
-/* cache, seqs (5), starts, keep, kept, stream */
+/* cache, device, page_table, starts, keep, cu_keep */
 static PyObject* kv_compact(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
-    int64_t v[10];
-    if (!ints(args, nargs, 10, 10, v)) return NULL;
-    const qmm_kv_seqs s = seqs_of(v + 1);
-    return PyLong_FromLong(g_kv.compact(PTR(const qmm_kv_cache*, v[0]), &s, PTR(const int32_t*, v[6]),
-                                        PTR(const int32_t*, v[7]), v[8], PTR(void*, v[9])));
+    ctx x;
+    DLTensor k;
+    qmm_kv_seqs s;
+    const int32_t* starts;
+    if (!begin(args, nargs, 6, &x) || !seqs_of(&x, args[2], args[3], "starts", args[5], "cu_keep", &s, &starts) ||
+        !vec(&x, args[4], "keep", -1, kDLInt, 32, &k) || !stream_of(&x))
+        return NULL;
+    return PyLong_FromLong(g_kv.compact(x.cache, &s, starts, (const int32_t*)data(&k), k.shape[0], x.stream));
 }
 
-/* cache, q, strides, o, strides, lse, seqs (5), lens, tokens, heads, window, tree, dtype, stream, scale */
+/* cache, device, q, page_table, lens, cu_tokens, o, lse, tree or None, window, scale */
 static PyObject* kv_attention(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
-    int64_t v[20];
-    if (!ints(args, nargs, 21, 20, v)) return NULL;
-    const double scale = PyFloat_AsDouble(args[20]);
-    if (scale == -1.0 && PyErr_Occurred()) return NULL;
-    const qmm_kv_seqs s = seqs_of(v + 8);
-    return PyLong_FromLong(g_kv.attention(PTR(const qmm_kv_cache*, v[0]), PTR(void*, v[1]), v[2], v[3], PTR(void*, v[4]), v[5],
-                                          v[6], PTR(float*, v[7]), &s, PTR(const int32_t*, v[13]), v[14], (int)v[15],
-                                          (float)scale, v[16], PTR(const int64_t*, v[17]), (qmm_dtype)v[18],
-                                          PTR(void*, v[19])));
+    ctx x;
+    rows q, o;
+    DLTensor l, tree;
+    qmm_kv_seqs s;
+    const int32_t* lens;
+    if (!begin(args, nargs, 11, &x) || !rows_of(&x, args[2], "q", &q) || !rows_of(&x, args[6], "out", &o)) return NULL;
+    if (!same_rows(&q, &o, "out must have q's shape and dtype")) return NULL;
+    if (!seqs_of(&x, args[3], args[4], "lens", args[5], "cu_tokens", &s, &lens) || !view(&x, args[7], "lse", 2, &l)) return NULL;
+    if (!is_type(&l, kDLFloat, 32) || l.shape[0] != q.tokens || l.shape[1] != q.heads ||
+        (l.strides && ((l.shape[1] > 1 && l.strides[1] != 1) || (l.shape[0] > 1 && l.strides[0] != l.shape[1])))) {
+        PyErr_SetString(PyExc_ValueError, "lse must be contiguous fp32 [tokens, heads]");
+        return NULL;
+    }
+    if (args[8] != Py_None && !vec(&x, args[8], "tree", q.tokens, kDLInt, 64, &tree)) return NULL;
+    const int64_t window = (int64_t)PyLong_AsLongLong(args[9]);
+    const double scale = PyFloat_AsDouble(args[10]);
+    if (PyErr_Occurred() || !stream_of(&x)) return NULL;
+    return PyLong_FromLong(g_kv.attention(x.cache, q.p, q.ts, q.hs, o.p, o.ts, o.hs, (float*)data(&l), &s, lens, q.tokens,
+                                          (int)q.heads, (float)scale, window,
+                                          args[8] == Py_None ? NULL : (const int64_t*)data(&tree), (qmm_dtype)q.dtype, x.stream));
 }
 
 static PyMethodDef methods[] = {
     {"bind", bind, METH_O, "bind(address of qmm_ex)"},
     {"qmm_ex", (PyCFunction)(void (*)(void))call, METH_FASTCALL,
      "qmm_ex(x, packed, scales, biases, y, M, N, K, bits, group, dtype, plan, stream) -> status"},
-    {"bind_kv", (PyCFunction)(void (*)(void))bind_kv, METH_FASTCALL, "addresses of the five K/V cache functions"},
+    {"bind_kv", (PyCFunction)(void (*)(void))bind_kv, METH_FASTCALL, "addresses of the five K/V cache functions, and the tensor type"},
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, "qmm_kv_append -> status"},
     {"kv_gather", (PyCFunction)(void (*)(void))kv_gather, METH_FASTCALL, "qmm_kv_gather -> status"},
     {"kv_copy_pages", (PyCFunction)(void (*)(void))kv_copy_pages, METH_FASTCALL, "qmm_kv_copy_pages -> status"},

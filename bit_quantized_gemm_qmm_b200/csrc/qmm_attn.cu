@@ -478,8 +478,10 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
         }
 
         // SUBS halves of a tile from its half h0 on; `there`: bit per half of the tile that was copied
-        auto part = [&](int t, uint32_t st, int h0, uint32_t there, auto masked_c) {
+        // COLS of the NT columns of query rows are in use
+        auto part = [&](int t, uint32_t st, int h0, uint32_t there, auto masked_c, auto cols_c) {
             constexpr bool MASKED = decltype(masked_c)::value;
+            constexpr int COLS = decltype(cols_c)::value;
             const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: this lane's row and piece
             const int kch = lane >> 4;
             // which of this lane's (position, query) pairs are seen
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                     const int tu = t + kAttnSub * (h0 + u) + g;
                     in[u][0] = ok && tu < cur->keys, in[u][1] = ok && tu + 8 < cur->keys;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < COLS; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int row = nt * 8 + 2 * c + (i & 1), p = tu + (i >> 1) * 8;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                 }
             }
             // ---- scores.  acc = sum over groups of b * sum(Q) (one MMA) + s * code sums
-            float acc[SUBS][NT][4], ks[SUBS][2][NG];
+            float acc[SUBS][COLS][4], ks[SUBS][2][NG];
 #pragma unroll
             for (int u = 0; u < SUBS; ++u) {
                 const uint32_t sb = st + 2 * F::CODES + (kAttnSub * (h0 + u) + g) * (2 * NG);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b1) : "r"(at + 16 * NG));
                     const uint32_t p0 = b0 * 0x10001u, p1 = b1 * 0x10001u;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < COLS; ++nt) {
                         const uint2 qb = NT == 1 ? qbreg[NT == 1 ? m : 0] : q_bias(nt, m);
                         if (m == 0) mma_16816_z(acc[u][nt], p0, p1, p0, p1, qb.x, qb.y);
                         else mma_16816(acc[u][nt], p0, p1, p0, p1, qb.x, qb.y);
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                 }
             }
             {
-                float sums[SUBS][NT][4];
+                float sums[SUBS][COLS][4];
                 uint32_t kw[SUBS][4];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                         const uint32_t e0 = w0 & 0x000F000Fu, e1 = w1 & 0x000F000Fu, e2 = y0 & 0x000F000Fu, e3 = y1 & 0x000F000Fu;
                         const uint32_t f0 = w0 & 0x00F000F0u, f1 = w1 & 0x00F000F0u, f2 = y0 & 0x00F000F0u, f3 = y1 & 0x00F000F0u;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                        for (int nt = 0; nt < COLS; ++nt) {
                             const uint4 q = NT == 1 ? qreg[NT == 1 ? ch : 0] : q_frag(nt, ch);
                             if (ch * 32 % GRP == 0) mma_16816_z(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
                             else mma_16816(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                         }
                         if ((ch + 1) * 32 % GRP == 0) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < COLS; ++nt)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     acc[u][nt][i] = fmaf(ks[u][i >> 1][ch * 32 / GRP], sums[u][nt][i], acc[u][nt][i]);
@@ -579,15 +581,15 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                     }
                 }
             }
-            float p[SUBS][NT][4];
-            uint32_t pk[SUBS][NT][NG][2];
+            float p[SUBS][COLS][4];
+            uint32_t pk[SUBS][COLS][NG][2];
             auto probabilities = [&]() -> bool {
                 uint32_t any = 0;
                 float top = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < SUBS; ++u)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < COLS; ++nt) {
                         const float2 qf = NT == 1 ? qfreg : q_factor(nt);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                         lg[u][k] = lg2(m) + 4.f;
                     }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < COLS; ++nt) {
                     const float2 qf = NT == 1 ? qfreg : q_factor(nt);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
 #pragma unroll
             for (int u = 0; u < SUBS; ++u)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < COLS; ++nt) {
                     l[nt][0] += p[u][nt][0] + p[u][nt][2];
                     l[nt][1] += p[u][nt][1] + p[u][nt][3];
 #pragma unroll
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                         f0 = hadd2_bits(f0, m80), f1 = hadd2_bits(f1, m80), f2 = hadd2_bits(f2, m80), f3 = hadd2_bits(f3, m80);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < COLS; ++nt) {
                         mma_16816(o[nt][ch][0], e0, e1, e2, e3, pk[u][nt][j][0], pk[u][nt][j][1]);
                         mma_16816(o[nt][ch][1], f0, f1, f2, f3, pk[u][nt][j][0], pk[u][nt][j][1]);
                     }
@@ -704,20 +706,26 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
 
         // ---- stream the tiles
         int slot = F::MS % F::RING;
-        const int full_lo = cur->full_lo, full_hi = cur->full_hi;
+        const int full_lo = cur->full_lo, full_hi = cur->full_hi, cols = (cur->rows + 7) / 8;
         for (int j = j0; j < j1; ++j) {
             sm100::cp_async_wait<F::RING - 2>();
             __syncwarp();
             issue(j + F::RING - 1, slot == 0 ? F::RING - 1 : slot - 1);
             const int t = t0 + kAttnUnit * W * j;
             const uint32_t there = (live >> (2 * slot)) & 3u, st = ring + slot * F::TILE;
-            if (there == 3 && t >= full_lo && t + kAttnUnit <= full_hi) {
+            auto tile = [&](auto cols_c) {
+                if (there == 3 && t >= full_lo && t + kAttnUnit <= full_hi) {
 #pragma unroll
-                for (int h0 = 0; h0 < 2; h0 += SUBS) part(t, st, h0, there, std::false_type{});
-            } else if (there) {
+                    for (int h0 = 0; h0 < 2; h0 += SUBS) part(t, st, h0, there, std::false_type{}, cols_c);
+                } else if (there) {
 #pragma unroll 1
-                for (int h0 = 0; h0 < 2; h0 += SUBS) part(t, st, h0, there, std::true_type{});
-            }
+                    for (int h0 = 0; h0 < 2; h0 += SUBS) part(t, st, h0, there, std::true_type{}, cols_c);
+                }
+            };
+            if (NT >= 4 && cols == 4) tile(std::integral_constant<int, NT >= 4 ? 4 : 1>{});
+            else if (NT >= 3 && cols == 3) tile(std::integral_constant<int, NT >= 3 ? 3 : 1>{});
+            else if (NT >= 2 && cols == 2) tile(std::integral_constant<int, NT >= 2 ? 2 : 1>{});
+            else tile(std::integral_constant<int, 1>{});
             slot = slot == F::RING - 1 ? 0 : slot + 1;
         }
         sm100::cp_async_wait<0>();
@@ -902,10 +910,11 @@ cudaError_t attn_resident(const AttnInst& k, int* out) {
 cudaError_t launch_attn(const AttnArgs& in, int head_dim, int group, cudaStream_t stream) {
     AttnArgs a = in;
     // query rows of a tile: the 8-row columns that the sequences' rows fill, so that the cache is
-    // streamed once wherever they fit.  Only the average is known here; where it is not a whole
-    // number the counts differ, and the longest are taken to have half as many tokens again
+    // streamed once wherever they fit.  Only the average is known here; where several sequences have
+    // several tokens, some are taken to have half as many again (columns that a tile does not fill
+    // cost next to nothing, but for the registers that more warps could have had)
     const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
-    const int64_t rows = (a.tokens % a.seqs ? mean + mean / 2 : mean) * a.group_heads;
+    const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
     const int64_t cols = (rows + 7) / 8, most = head_dim == 256 ? 2 : 4;
     const AttnInst k = instance(head_dim, group, int(cols < most ? cols : most));
     int blocks = 0;

@@ -46,48 +46,42 @@ __device__ __forceinline__ int64_t cache_row(const KvArgs& a, int b, int pos, in
     return (int64_t(page) * a.kv_heads + h) * a.page + (pos - col * a.page);
 }
 
-// ---------------------------------------------------------------- append
-// One thread a word (eight values); a group's range is found by its GRP / 8 lanes.  Each step is
-// the scheme of qmm_quant.cu, rounded the same way, so the bits are those of qmm_quantize (its scan
-// keeps the first of equal extremes, which decides the sign of a zero: so does this one).  A group
-// with an infinity or NaN, or whose scale or bias leaves fp16, is stored so that it reads as NaN.
-template <int GRP>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ KvArgs a) {
-    const int per = a.dim / 8;
+// A thread's word (eight values) of the token axis: token, head and place in the row.  Row counts stay
+// below 2^28 (2^20 tokens, 256 heads), so only the word number needs 64 bits.
+struct Word {
+    int tok, h, p8;
+    bool on;
+};
+__device__ __forceinline__ Word my_word(const KvArgs& a) {
+    const int lg = a.dim == 64 ? 3 : a.dim == 128 ? 4 : 5;
     const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t row = i / per;
-    const int p8 = int(i - row * per), lane = threadIdx.x & 31;
-    const bool is_v = blockIdx.y != 0;
-    const bool on = row < int64_t(a.tokens) * a.kv_heads;
-    const int tok = on ? int(row / a.kv_heads) : a.tokens - 1, h = on ? int(row - int64_t(tok) * a.kv_heads) : 0;
-    grid_dependency_wait();
-    grid_dependents_launch();
+    const int row = int(i >> lg);
+    Word w;
+    w.on = row < a.tokens * a.kv_heads;
+    w.p8 = int(i) & ((1 << lg) - 1);
+    w.tok = w.on ? row / a.kv_heads : a.tokens - 1;
+    w.h = w.on ? row - w.tok * a.kv_heads : 0;
+    return w;
+}
+
+// ---------------------------------------------------------------- append
+// One thread the same eight values of K and of V; a group's range is found by its GRP / 8 lanes.  Each
+// step is the scheme of qmm_quant.cu, rounded the same way, so the bits are those of qmm_quantize (its
+// scan keeps the first of equal extremes, which decides the sign of a zero: so does this one).  A group
+// with an infinity or NaN, or whose scale or bias leaves fp16, is stored so that it reads as NaN.
+struct Quantized {
+    uint32_t word;
+    uint16_t s, b;
+};
+template <int GRP>
+__device__ __forceinline__ Quantized quantize_word(uint4 u, int is_bf16) {
+    const int lane = threadIdx.x & 31;
     float v[8];
-    {
-        const uint16_t* src = is_v ? a.v + int64_t(tok) * a.v_ts + int64_t(h) * a.v_hs
-                                   : a.k + int64_t(tok) * a.k_ts + int64_t(h) * a.k_hs;
-        src += p8 * 8;
-        uint32_t raw[4];
-        if (a.vec) {
-            const uint4 u = ldg_stream_v4(src);
-            raw[0] = u.x, raw[1] = u.y, raw[2] = u.z, raw[3] = u.w;
-        } else {
+    const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) raw[j] = uint32_t(src[2 * j]) | uint32_t(src[2 * j + 1]) << 16;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = a.is_bf16 ? bf16lo_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j])));
-            v[2 * j + 1] = a.is_bf16 ? bf16hi_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j] >> 16)));
-        }
-    }
-    const int b = seq_of(a.cu, a.seqs, tok);
-    int64_t at = -1;
-    bool bad = false;
-    if (on && b < a.seqs && a.cu[b] <= tok) {  // rows in front of the first or behind the last sequence are left
-        const AttnSeq s = attn_seq(a.cu[b], a.cu[b + 1], a.at[b], a.tokens, a.capacity, 1, 1, 0);
-        at = cache_row(a, b, s.start + (tok - s.row0), h);
-        bad = at < 0;
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = is_bf16 ? bf16lo_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j])));
+        v[2 * j + 1] = is_bf16 ? bf16hi_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j] >> 16)));
     }
     float lo = v[0], hi = v[0];
     bool odd = false;
@@ -106,80 +100,146 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
     const unsigned group_lanes = ((1u << (GRP / 8)) - 1u) << (lane & ~(GRP / 8 - 1));
     odd = (__ballot_sync(kFull, odd) & group_lanes) != 0;
-    uint16_t sh = __half_as_ushort(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
-    uint16_t bh = __half_as_ushort(__float2half_rn(lo));
-    odd |= (sh & 0x7C00) == 0x7C00 || (bh & 0x7C00) == 0x7C00;
-    if (odd) sh = bh = 0x7FFF;
-    const float s = __half2float(__ushort_as_half(sh)), bf = __half2float(__ushort_as_half(bh));
-    uint32_t word = 0;
+    Quantized r;
+    r.s = __half_as_ushort(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
+    r.b = __half_as_ushort(__float2half_rn(lo));
+    odd |= (r.s & 0x7C00) == 0x7C00 || (r.b & 0x7C00) == 0x7C00;
+    if (odd) r.s = r.b = 0x7FFF;
+    const float s = __half2float(__ushort_as_half(r.s)), bf = __half2float(__ushort_as_half(r.b));
+    r.word = 0;
     if (!odd && s != 0.f) {
+        // rint(RN(d / s)) from d * RN(1 / s), which is within 2^-22 of d / s in relative terms (two
+        // roundings): it has the same nearest whole number unless it lies within 2^-12 of a half (codes
+        // are clamped at 15, so only quotients below 16 matter); there the division itself decides
+        const float inv = __frcp_rn(s);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int q = __float2int_rn(__fdiv_rn(__fsub_rn(v[j], bf), s));
-            word |= uint32_t(clamp_int(q, 0, 15)) << (4 * j);
+            const float d = __fsub_rn(v[j], bf);
+            float t = d * inv;
+            const float f = t - floorf(t);
+            if (fabsf(f - 0.5f) < 0.000244140625f) t = __fdiv_rn(d, s);
+            r.word |= uint32_t(clamp_int(__float2int_rn(t), 0, 15)) << (4 * j);
         }
     }
-    flag_bad(bad);
+    return r;
+}
+
+template <int GRP>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ KvArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const Word w = my_word(a);
+    const uint16_t* ksrc = a.k + int64_t(w.tok) * a.k_ts + int64_t(w.h) * a.k_hs + w.p8 * 8;
+    const uint16_t* vsrc = a.v + int64_t(w.tok) * a.v_ts + int64_t(w.h) * a.v_hs + w.p8 * 8;
+    uint4 kraw, vraw;
+    if (a.vec) {
+        kraw = ldg_stream_v4(ksrc);
+        vraw = ldg_stream_v4(vsrc);
+    } else {
+        auto load = [](const uint16_t* p) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = uint32_t(p[2 * j]) | uint32_t(p[2 * j + 1]) << 16;
+            return make_uint4(u[0], u[1], u[2], u[3]);
+        };
+        kraw = load(ksrc);
+        vraw = load(vsrc);
+    }
+    const int b = seq_of(a.cu, a.seqs, w.tok);
+    int64_t at = -1;
+    if (w.on && b < a.seqs && a.cu[b] <= w.tok) {  // rows in front of the first or behind the last sequence are left
+        const AttnSeq s = attn_seq(a.cu[b], a.cu[b + 1], a.at[b], a.tokens, a.capacity, 1, 1, 0);
+        at = cache_row(a, b, s.start + (w.tok - s.row0), w.h);
+        flag_bad(at < 0);
+    }
+    const Quantized k = quantize_word<GRP>(kraw, a.is_bf16), v = quantize_word<GRP>(vraw, a.is_bf16);
     if (at < 0) return;
-    (is_v ? a.vc : a.kc)[at * per + p8] = word;
-    if (p8 % (GRP / 8) == 0) {
-        const int64_t gi = at * (a.dim / GRP) + p8 / (GRP / 8);
-        (is_v ? a.vs : a.ks)[gi] = sh;
-        (is_v ? a.vb : a.kb)[gi] = bh;
+    const int64_t word = at * (a.dim / 8) + w.p8;
+    a.kc[word] = k.word;
+    a.vc[word] = v.word;
+    if (w.p8 % (GRP / 8) == 0) {
+        const int64_t gi = word / (GRP / 8);
+        a.ks[gi] = k.s, a.kb[gi] = k.b;
+        a.vs[gi] = v.s, a.vb[gi] = v.b;
     }
 }
 
 // ---------------------------------------------------------------- gather
-// One thread a word: RNE_out(RN_fp32(s * q + b)), the values qmm_dequantize gives.
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ KvArgs a) {
-    const int per = a.dim / 8;
-    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t row = i / per;
-    const int p8 = int(i - row * per);
-    const bool is_v = blockIdx.y != 0;
-    const bool on = row < int64_t(a.tokens) * a.kv_heads;
-    const int tok = on ? int(row / a.kv_heads) : a.tokens - 1, h = on ? int(row - int64_t(tok) * a.kv_heads) : 0;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const int b = seq_of(a.cu, a.seqs, tok);
-    if (!on || b >= a.seqs) return;
-    const int c0 = clamp_int(a.cu[b], 0, a.tokens);
-    if (tok < c0) return;
-    const int64_t at = cache_row(a, b, a.at[b] + (tok - c0), h);
-    uint32_t out[4] = {0, 0, 0, 0};
-    if (at >= 0) {
-        const uint32_t word = (is_v ? a.vc : a.kc)[at * per + p8];
-        const int64_t gi = at * (a.dim / a.group) + p8 / (a.group / 8);
-        const float s = __half2float(__ushort_as_half((is_v ? a.vs : a.ks)[gi]));
-        const float bb = __half2float(__ushort_as_half((is_v ? a.vb : a.kb)[gi]));
+// One thread a word of K and of V: RNE_out(RN_fp32(s * q + b)), the values qmm_dequantize gives.
+__device__ __forceinline__ uint4 dequantize_word(uint32_t word, uint16_t sh, uint16_t bh, int is_bf16) {
+    const float s = __half2float(__ushort_as_half(sh)), b = __half2float(__ushort_as_half(bh));
+    uint32_t out[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = __fmaf_rn(s, float((word >> (8 * j)) & 15), bb);
-            const float y = __fmaf_rn(s, float((word >> (8 * j + 4)) & 15), bb);
-            if (a.is_bf16) {
-                const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
-                out[j] = *reinterpret_cast<const uint32_t*>(&t);
-            } else {
-                out[j] = f32x2_to_f16x2(x, y);
-            }
+    for (int j = 0; j < 4; ++j) {
+        const float x = __fmaf_rn(s, float((word >> (8 * j)) & 15), b);
+        const float y = __fmaf_rn(s, float((word >> (8 * j + 4)) & 15), b);
+        if (is_bf16) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+            out[j] = *reinterpret_cast<const uint32_t*>(&t);
+        } else {
+            out[j] = f32x2_to_f16x2(x, y);
         }
     }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ KvArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const Word w = my_word(a);
+    const int b = seq_of(a.cu, a.seqs, w.tok);
+    if (!w.on || b >= a.seqs) return;
+    const int c0 = clamp_int(a.cu[b], 0, a.tokens);
+    if (w.tok < c0) return;
+    const int64_t at = cache_row(a, b, a.at[b] + (w.tok - c0), w.h);
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (at >= 0) {
+        const int64_t word = at * (a.dim / 8) + w.p8;
+        const int64_t gi = a.group == 32 ? word >> 2 : a.group == 64 ? word >> 3 : word >> 4;
+        const uint32_t kw = a.kc[word], vw = a.vc[word];
+        const uint16_t ks = a.ks[gi], kb = a.kb[gi], vs = a.vs[gi], vb = a.vb[gi];
+        k = dequantize_word(kw, ks, kb, a.is_bf16);
+        v = dequantize_word(vw, vs, vb, a.is_bf16);
+    }
     flag_bad(at < 0);
-    uint16_t* dst = is_v ? a.v_out + int64_t(tok) * a.v_ts + int64_t(h) * a.v_hs
-                         : a.k_out + int64_t(tok) * a.k_ts + int64_t(h) * a.k_hs;
-    *reinterpret_cast<uint4*>(dst + p8 * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>(a.k_out + int64_t(w.tok) * a.k_ts + int64_t(w.h) * a.k_hs + w.p8 * 8) = k;
+    *reinterpret_cast<uint4*>(a.v_out + int64_t(w.tok) * a.v_ts + int64_t(w.h) * a.v_hs + w.p8 * 8) = v;
 }
 
 // ---------------------------------------------------------------- copy pages
 // One pair of pages by gridDim.y blocks, each an even part of the six arrays' 16-byte pieces (a
-// page is contiguous in each).  A pair whose target is a later pair's too is left to that one; a
-// pair whose source is another pair's target has no defined answer and is skipped as an error.
+// page is contiguous in each), at most kCopy a thread: all of them are loaded before the pairs are
+// looked through.  A pair whose target is a later pair's too is left to that one; a pair whose source
+// is another pair's target has no defined answer and is skipped as an error.
+constexpr int kCopy = 9;
 __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ KvArgs a, const int32_t* src,
                                                         const int32_t* dst, int pairs) {
     grid_dependency_wait();
     grid_dependents_launch();
     const int i = blockIdx.x;
     const int from = src[i], to = dst[i];
+    bool bad = from < 0 || from >= a.pages || to < 0 || to >= a.pages;
+    const int rows = a.kv_heads * a.page;
+    const int cp = rows * (a.dim / 32), sp = rows * (a.dim / a.group) / 8;  // 16-byte pieces of a page
+    const int all = 2 * cp + 4 * sp;
+    const int p0 = int(int64_t(all) * blockIdx.y / gridDim.y), p1 = int(int64_t(all) * (blockIdx.y + 1) / gridDim.y);
+    // where piece p of page `page` is
+    auto at = [&](int p, int page) {
+        const bool codes = p < 2 * cp;
+        const int n = codes ? cp : sp, q = codes ? p : p - 2 * cp;
+        const int k = (q >= n) + (q >= 2 * n) + (q >= 3 * n);
+        uint32_t* const c = k ? a.vc : a.kc;
+        uint16_t* const s = k == 0 ? a.ks : k == 1 ? a.kb : k == 2 ? a.vs : a.vb;
+        return reinterpret_cast<uint4*>(codes ? static_cast<void*>(c) : static_cast<void*>(s)) + int64_t(page) * n + (q - k * n);
+    };
+    uint4 v[kCopy];
+    if (!bad) {
+#pragma unroll
+        for (int j = 0; j < kCopy; ++j) {
+            const int p = p0 + j * kThreads + threadIdx.x;
+            if (p < p1) v[j] = *at(p, from);
+        }
+    }
     bool later = false, torn = false;
     for (int j = threadIdx.x; j < pairs; j += kThreads) {
         const int d = dst[j];
@@ -188,31 +248,13 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
     }
     later = __syncthreads_or(later);
     torn = __syncthreads_or(torn);
-    const bool bad = from < 0 || from >= a.pages || to < 0 || to >= a.pages || (torn && from != to);
+    bad |= torn && from != to;
     if (threadIdx.x == 0 && blockIdx.y == 0) flag_bad(bad);
     if (bad || later || from == to) return;
-    const int64_t rows = int64_t(a.kv_heads) * a.page;
-    const int64_t cp = rows * a.dim / 32, sp = rows * (a.dim / a.group) / 8;  // 16-byte pieces of a page
-    const int64_t all = 2 * cp + 4 * sp;
-    const int64_t p0 = all * blockIdx.y / gridDim.y, p1 = all * (blockIdx.y + 1) / gridDim.y;
-    uint16_t* const arr[6] = {reinterpret_cast<uint16_t*>(a.kc), reinterpret_cast<uint16_t*>(a.vc), a.ks, a.kb, a.vs, a.vb};
-    int64_t base = 0;
 #pragma unroll
-    for (int k = 0; k < 6; ++k) {
-        const int64_t n = k < 2 ? cp : sp;
-        const int64_t lo = p0 > base ? p0 - base : 0, hi = p1 - base < n ? p1 - base : n;
-        const uint4* s = reinterpret_cast<const uint4*>(arr[k]) + int64_t(from) * n;
-        uint4* d = reinterpret_cast<uint4*>(arr[k]) + int64_t(to) * n;
-        int64_t p = lo + threadIdx.x;
-        for (; p + 3 * kThreads < hi; p += 4 * kThreads) {
-            uint4 v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = s[p + j * kThreads];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[p + j * kThreads] = v[j];
-        }
-        for (; p < hi; p += kThreads) d[p] = s[p];
-        base += n;
+    for (int j = 0; j < kCopy; ++j) {
+        const int p = p0 + j * kThreads + threadIdx.x;
+        if (p < p1) *at(p, to) = v[j];
     }
 }
 
@@ -221,14 +263,16 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
 // another; further ones (in rising order, so they lie behind all that is written) follow.
 constexpr int kKeep = 64;
 __global__ void __launch_bounds__(128) compact_kernel(const __grid_constant__ KvArgs a, const int32_t* keep, int kept) {
-    __shared__ uint4 codes[2 * kKeep * 8];
-    __shared__ uint16_t consts[4 * kKeep * 8];
+    extern __shared__ uint4 codes[];  // K's, then V's: [kKeep][dim / 32] pieces each; then the constants
     __shared__ int64_t from[kKeep], to[kKeep];
     const int b = blockIdx.x, h = blockIdx.y, t = threadIdx.x;
     grid_dependency_wait();
     grid_dependents_launch();
     const int k0 = clamp_int(a.cu[b], 0, kept), k1 = clamp_int(a.cu[b + 1], 0, kept), first = a.at[b];
     const int vec = a.dim / 32, ng = a.dim / a.group;
+    uint4* const vcodes = codes + kKeep * vec;
+    uint16_t* const consts = reinterpret_cast<uint16_t*>(vcodes + kKeep * vec);
+    const int cs = kKeep * ng;
     for (int j0 = k0; j0 < k1; j0 += kKeep) {
         const int n = k1 - j0 < kKeep ? k1 - j0 : kKeep;
         if (t < n) {
@@ -244,28 +288,28 @@ __global__ void __launch_bounds__(128) compact_kernel(const __grid_constant__ Kv
             const int r = i / vec, p = i - r * vec;
             if (from[r] < 0) continue;
             codes[i] = reinterpret_cast<const uint4*>(a.kc)[from[r] * vec + p];
-            codes[kKeep * 8 + i] = reinterpret_cast<const uint4*>(a.vc)[from[r] * vec + p];
+            vcodes[i] = reinterpret_cast<const uint4*>(a.vc)[from[r] * vec + p];
         }
         for (int i = t; i < n * ng; i += 128) {
             const int r = i / ng, p = i - r * ng;
             if (from[r] < 0) continue;
             const int64_t at = from[r] * ng + p;
-            consts[i] = a.ks[at], consts[kKeep * 8 + i] = a.kb[at];
-            consts[2 * kKeep * 8 + i] = a.vs[at], consts[3 * kKeep * 8 + i] = a.vb[at];
+            consts[i] = a.ks[at], consts[cs + i] = a.kb[at];
+            consts[2 * cs + i] = a.vs[at], consts[3 * cs + i] = a.vb[at];
         }
         __syncthreads();
         for (int i = t; i < n * vec; i += 128) {
             const int r = i / vec, p = i - r * vec;
             if (from[r] < 0) continue;
             reinterpret_cast<uint4*>(a.kc)[to[r] * vec + p] = codes[i];
-            reinterpret_cast<uint4*>(a.vc)[to[r] * vec + p] = codes[kKeep * 8 + i];
+            reinterpret_cast<uint4*>(a.vc)[to[r] * vec + p] = vcodes[i];
         }
         for (int i = t; i < n * ng; i += 128) {
             const int r = i / ng, p = i - r * ng;
             if (from[r] < 0) continue;
             const int64_t at = to[r] * ng + p;
-            a.ks[at] = consts[i], a.kb[at] = consts[kKeep * 8 + i];
-            a.vs[at] = consts[2 * kKeep * 8 + i], a.vb[at] = consts[3 * kKeep * 8 + i];
+            a.ks[at] = consts[i], a.kb[at] = consts[cs + i];
+            a.vs[at] = consts[2 * cs + i], a.vb[at] = consts[3 * cs + i];
         }
         __syncthreads();
     }
@@ -291,27 +335,23 @@ unsigned word_blocks(const KvArgs& a) {
 
 cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a), 2), kThreads, stream, &attr);
+    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a)), kThreads, stream, &attr);
     return cudaLaunchKernelEx(&cfg, a.group == 32 ? append_kernel<32> : a.group == 64 ? append_kernel<64> : append_kernel<128>, a);
 }
 
 cudaError_t launch_kv_gather(const KvArgs& a, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a), 2), kThreads, stream, &attr);
+    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a)), kThreads, stream, &attr);
     return cudaLaunchKernelEx(&cfg, gather_kernel, a);
 }
 
 cudaError_t launch_kv_copy_pages(const KvArgs& a, const int32_t* src, const int32_t* dst, int pairs, cudaStream_t stream) {
-    // about 16 pieces a thread, in more blocks a pair while the pairs alone do not fill the SMs
+    // at most kCopy pieces a thread, in more blocks a pair while the pairs alone do not fill the SMs
     const int64_t rows = int64_t(a.kv_heads) * a.page;
     const int64_t pieces = rows * (a.dim / 16) + rows * (a.dim / a.group) / 2;
-    int64_t parts = (pieces + 16 * kThreads - 1) / (16 * kThreads);
-    const int64_t fill = (148 * 4 + pairs - 1) / pairs;
-    if (parts < fill) parts = fill;
-    const int64_t most = (pieces + kThreads - 1) / kThreads;
-    if (parts > most) parts = most;
-    if (parts < 1) parts = 1;
-    if (parts > 65535) parts = 65535;
+    int64_t parts = (pieces + kCopy * kThreads - 1) / (kCopy * kThreads);
+    const int64_t fill = (148 * 4 + pairs - 1) / pairs, most = (pieces + kThreads - 1) / kThreads;
+    if (parts < fill) parts = fill < most ? fill : most;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(dim3(unsigned(pairs), unsigned(parts)), kThreads, stream, &attr);
     return cudaLaunchKernelEx(&cfg, copy_kernel, a, src, dst, pairs);
@@ -319,7 +359,8 @@ cudaError_t launch_kv_copy_pages(const KvArgs& a, const int32_t* src, const int3
 
 cudaError_t launch_kv_compact(const KvArgs& a, const int32_t* keep, int kept, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(dim3(unsigned(a.seqs), unsigned(a.kv_heads)), 128, stream, &attr);
+    cudaLaunchConfig_t cfg = config(dim3(unsigned(a.seqs), unsigned(a.kv_heads)), 128, stream, &attr);
+    cfg.dynamicSmemBytes = size_t(kKeep) * (a.dim + 8 * (a.dim / a.group));
     return cudaLaunchKernelEx(&cfg, compact_kernel, a, keep, kept);
 }
 

@@ -61,19 +61,26 @@ QMM_HD int attn_seq_units(const AttnSeq& s, int kv_heads) { return attn_seq_item
 
 QMM_HD int ceil_div_int(int a, int b) { return (a - 1) / b + 1; }  // a >= 1
 
-// How the work is dealt out over `blocks` blocks.  Few items: each is cut into pieces of `per` units (the
-// last one shorter), one a block, so that no block has to change items; the pieces are as small as
-// keeps their number within the blocks, and give each of a block's warps a unit at least.  Many items:
-// block i takes units [i * per, (i + 1) * per) of all, across items.
+// How the work is dealt out over `blocks` blocks.  Even shares: block i takes units [i * per,
+// (i + 1) * per) of all, across items; a block whose share holds the end of one item and the start of
+// the next changes items, which costs about as much as kAttnChange units.  Pieces, where items are
+// few: each item is cut into pieces of `per` units (the last one shorter), one a block, so that no
+// block changes items; the pieces are as small as keeps their number within the blocks, and give each
+// of a block's warps a unit at least.
+constexpr int kAttnChange = 12;
 struct AttnPlan {
     int total, per, pieces;  // units of all; units a block; 1: pieces
 };
 QMM_HD AttnPlan attn_plan(int total, int items, int blocks, int warps) {
     AttnPlan p;
     p.total = total;
-    p.pieces = items <= blocks / 2;
-    p.per = total < 1 ? 1 : ceil_div_int(total, p.pieces ? blocks - items : blocks);
-    if (p.pieces && p.per < warps) p.per = warps;
+    p.pieces = 0;
+    p.per = total < 1 ? 1 : ceil_div_int(total, blocks);
+    if (total > 0 && items < blocks) {
+        int piece = ceil_div_int(total, blocks - items);
+        if (piece < warps) piece = warps;
+        if (piece <= p.per + kAttnChange) p.pieces = 1, p.per = piece;
+    }
     return p;
 }
 

@@ -43,7 +43,7 @@ class KVCache:
                 raise ValueError(f"{name} must be contiguous {kind} {list(want)}, got {t.dtype} {list(t.shape)}")
             setattr(self, name, t)
         self.pages, self.kv_heads, self.page_size, self.head_dim, self.group = pages, heads, page, dim, group
-        self.device = k_packed.device
+        self.device, self.scale = k_packed.device, dim ** -0.5
         self._index = k_packed.get_device()
         self._desc = _q.CacheDesc(*(t.data_ptr() for t in arrays), pages, page, heads, dim, group, 4, 0)
         self._addr = ctypes.addressof(self._desc)
@@ -67,10 +67,12 @@ class KVCache:
 
 
 _call = None
+_device = torch._C._cuda_getDevice
 
 
 def _calls():
-    """The C hand-off module, bound to the loaded library's functions."""
+    """The C hand-off module, bound to the loaded library's functions.  It checks the tensors (device,
+    dtype, shape, strides) and passes them on with the device's current stream."""
     global _call
     if _call is None:
         L = _q.lib()
@@ -79,53 +81,20 @@ def _calls():
         except ImportError as e:
             raise _q.QmmUnavailable(f"the _qmm_call module is missing ({e}); run __graft_entry__.build()") from e
         _qmm_call.bind_kv(*(ctypes.cast(getattr(L, "qmm_kv_" + n), ctypes.c_void_p).value
-                            for n in ("append", "gather", "copy_pages", "compact", "attention")))
+                            for n in ("append", "gather", "copy_pages", "compact", "attention")), torch.Tensor)
         _call = _qmm_call
     return _call
 
 
 def _run(cache: KVCache, fn, *args) -> None:
     """One hand-off, on the cache's device; a status other than OK is raised."""
-    dev = cache._index
-    if dev == torch.cuda.current_device():
-        st = fn(*args)
+    if cache._index == _device():
+        st = fn(cache._addr, cache._index, *args)
     else:  # the library launches on the calling thread's current device
-        with torch.cuda.device(dev):
-            st = fn(*args)
+        with torch.cuda.device(cache._index):
+            st = fn(cache._addr, cache._index, *args)
     if st:
         _q._check(st)
-
-
-def _ints(cache: KVCache, t: torch.Tensor, n: int, what: str) -> int:
-    """Address of a contiguous int32 vector of n values on the cache's device."""
-    if t.dtype is not torch.int32 or t.get_device() != cache._index or t.dim() != 1 or t.numel() != n \
-            or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous int32 vector of {n} values on the cache's device")
-    return t.data_ptr()
-
-
-def _seqs(cache: KVCache, table: torch.Tensor, cu: torch.Tensor):
-    """(table, row stride, columns, sequences, offsets) of the C call."""
-    if table.dtype is not torch.int32 or table.dim() != 2 or table.get_device() != cache._index:
-        raise ValueError("page_table must be an int32 [seqs, pages] tensor on the cache's device")
-    n, cols = table.shape
-    row, col = table.stride()
-    if cols > 1 and col != 1:
-        raise ValueError("a row of page_table must be contiguous")
-    return table.data_ptr(), row if n > 1 else cols, cols, n, _ints(cache, cu, n + 1, "cu_tokens")
-
-
-def _rows(cache: KVCache, t: torch.Tensor, what: str):
-    """(address, token stride, head stride, tokens, heads) of a [tokens, heads, head_dim] tensor."""
-    if t.dim() != 3 or t.get_device() != cache._index:
-        raise ValueError(f"{what} must be a [tokens, heads, head_dim] tensor on the cache's device")
-    n, h, d = t.shape
-    if d != cache.head_dim:
-        raise ValueError(f"{what} has rows of {d} values; the cache's head_dim is {cache.head_dim}")
-    ts, hs, ds = t.stride()
-    if ds != 1:
-        raise ValueError(f"the last dimension of {what} must be contiguous")
-    return t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0, n, h
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
@@ -133,13 +102,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torc
     """Quantizes new tokens' K and V rows ([tokens, kv_heads, head_dim], any token and head strides)
     into the cache.  lens counts each sequence's tokens with the new ones, which are its last; rows
     cu_tokens[b]..cu_tokens[b+1]-1 are sequence b's."""
-    kp, kts, khs, n, h = _rows(cache, k, "k")
-    vp, vts, vhs, nv, hv = _rows(cache, v, "v")
-    if h != cache.kv_heads or hv != h or nv != n or v.dtype is not k.dtype:
-        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
-    seqs = _seqs(cache, page_table, cu_tokens)
-    _run(cache, _calls().kv_append, cache._addr, kp, kts, khs, vp, vts, vhs, *seqs, _ints(cache, lens, seqs[3], "lens"), n,
-         _q._dtype_code(k.dtype), _q._current_stream(cache._index))
+    _run(cache, _calls().kv_append, k, v, page_table, lens, cu_tokens)
 
 
 def kv_gather(cache: KVCache, page_table: torch.Tensor, starts: torch.Tensor, cu_tokens: torch.Tensor, tokens: int,
@@ -147,35 +110,27 @@ def kv_gather(cache: KVCache, page_table: torch.Tensor, starts: torch.Tensor, cu
     """Cache rows as dense (k, v) [tokens, kv_heads, head_dim]: rows cu_tokens[b] + i are positions
     starts[b] + i of sequence b.  Rows of no sequence are left as they are."""
     if out is None:
-        shape = (tokens, cache.kv_heads, cache.head_dim)
-        out = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
-    k, v = out
-    kp, kts, khs, n, h = _rows(cache, k, "out[0]")
-    vp, vts, vhs, nv, hv = _rows(cache, v, "out[1]")
-    if (n, h) != (tokens, cache.kv_heads) or (nv, hv) != (n, h) or k.dtype is not dtype or v.dtype is not dtype:
-        raise ValueError("out must be two [tokens, kv_heads, head_dim] tensors of dtype")
-    seqs = _seqs(cache, page_table, cu_tokens)
-    _run(cache, _calls().kv_gather, cache._addr, *seqs, _ints(cache, starts, seqs[3], "starts"), n, kp, kts, khs, vp, vts,
-         vhs, _q._dtype_code(dtype), _q._current_stream(cache._index))
+        both = torch.empty((2, tokens, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
+        k, v = both[0], both[1]
+    else:
+        k, v = out
+        if k.shape[0] != tokens or k.dtype is not dtype:
+            raise ValueError("out must be two [tokens, kv_heads, head_dim] tensors of dtype")
+    _run(cache, _calls().kv_gather, k, v, page_table, starts, cu_tokens)
     return k, v
 
 
 def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Page dst[i] becomes a copy of page src[i] (all heads, K and V).  No page may be one pair's
     source and another's target; of pairs with one target the last counts."""
-    n = src.numel()
-    _run(cache, _calls().kv_copy_pages, cache._addr, _ints(cache, src, n, "src"), _ints(cache, dst, n, "dst"), n,
-         _q._current_stream(cache._index))
+    _run(cache, _calls().kv_copy_pages, src, dst)
 
 
 def kv_compact(cache: KVCache, page_table: torch.Tensor, starts: torch.Tensor, keep: torch.Tensor,
                cu_keep: torch.Tensor) -> None:
     """Moves accepted draft rows together: entries cu_keep[b]..cu_keep[b+1]-1 of keep, rising, are
     offsets from starts[b] of the rows of sequence b that become rows starts[b], starts[b] + 1, ..."""
-    seqs = _seqs(cache, page_table, cu_keep)
-    n = keep.numel()
-    _run(cache, _calls().kv_compact, cache._addr, *seqs, _ints(cache, starts, seqs[3], "starts"),
-         _ints(cache, keep, n, "keep"), n, _q._current_stream(cache._index))
+    _run(cache, _calls().kv_compact, page_table, starts, keep, cu_keep)
 
 
 def kv_attention(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, cu_tokens: torch.Tensor,
@@ -186,27 +141,13 @@ def kv_attention(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lens
     `window` positions up to its own.  tree: int64 [tokens], bit j of a token's mask set where it sees
     its sequence's new token j (and every position before the new ones).  o has q's dtype; lse is fp32
     [tokens, heads], -inf where a row sees nothing.  Rows of no sequence are left as they are."""
-    qp, qts, qhs, n, heads = _rows(cache, q, "q")
+    shape = q.shape
     if out is None:
-        out = torch.empty((n, heads, cache.head_dim), dtype=q.dtype, device=cache.device)
-    op, ots, ohs, no, ho = _rows(cache, out, "out")
-    if no != n or ho != heads or out.dtype is not q.dtype:
-        raise ValueError("out must be [tokens, heads, head_dim] of q's dtype")
+        out = torch.empty(shape, dtype=q.dtype, device=cache.device)
     if lse is None:
-        lse = torch.empty((n, heads), dtype=torch.float32, device=cache.device)
-    elif lse.dtype is not torch.float32 or tuple(lse.shape) != (n, heads) or not lse.is_contiguous() \
-            or lse.get_device() != cache._index:
-        raise ValueError("lse must be a contiguous fp32 [tokens, heads] tensor on the cache's device")
-    bits = 0
-    if tree is not None:
-        if tree.dtype is not torch.int64 or tree.dim() != 1 or tree.numel() != n or not tree.is_contiguous() \
-                or tree.get_device() != cache._index:
-            raise ValueError("tree must be a contiguous int64 vector of one mask a token on the cache's device")
-        bits = tree.data_ptr()
-    seqs = _seqs(cache, page_table, cu_tokens)
-    _run(cache, _calls().kv_attention, cache._addr, qp, qts, qhs, op, ots, ohs, lse.data_ptr(), *seqs,
-         _ints(cache, lens, seqs[3], "lens"), n, heads, window, bits, _q._dtype_code(q.dtype),
-         _q._current_stream(cache._index), cache.head_dim ** -0.5 if scale is None else scale)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=cache.device)
+    _run(cache, _calls().kv_attention, q, page_table, lens, cu_tokens, out, lse, tree, window,
+         cache.scale if scale is None else scale)
     return out, lse
 
 
@@ -336,8 +277,9 @@ class KVSequences:
         their attention [tokens, heads, head_dim]."""
         if len(set(seqs)) != len(seqs) or len(new) != len(seqs) or sum(new) != q.shape[0] or min(new, default=0) < 0:
             raise ValueError("seqs must be different sequences, new their counts of the rows")
-        for t, what in ((q, "q"), (k, "k"), (v, "v")):
-            _rows(self.cache, t, what)
+        for t in (q, k, v):
+            if t.dim() != 3 or t.shape[0] != q.shape[0] or t.shape[2] != self.cache.head_dim or t.dtype is not q.dtype:
+                raise ValueError("q, k and v must be [tokens, heads, head_dim] of one dtype")
         page = self.cache.page_size
         need = [-(-(self._lens[s] + n) // page) - len(self._pages[s]) for s, n in zip(seqs, new)]
         got = self._take(sum(need))

@@ -224,30 +224,24 @@ def test_refuses_other_arguments(L):
     assert L.qmm_kv_copy_pages(r(c), 0, 0, 0, None) == 0 and L.qmm_kv_compact(r(c), r(s), 0, 0, 0, None) == 0
 
 
-def test_call_module_forwards(L):
-    """The C hand-off passes every argument on: the library's statuses, and its own refusals."""
+def test_call_module_refuses(L):
+    """The C hand-off looks at every tensor before it calls: types, counts of arguments, devices."""
     m = kv._calls()
-    good, bad = cache(), cache(bits=8)
-    s = (16, 3, 3, 0, 16)  # no sequences: nothing is launched
-    for c, want in ((good, 0), (bad, 2)):
-        a = ctypes.addressof(c)
-        assert m.kv_append(a, 16, 1, 1, 16, 1, 1, *s, 16, 2, 0, 0) == want
-        assert m.kv_gather(a, *s, 16, 2, 16, 8, 8, 16, 8, 8, 0, 0) == want
-        assert m.kv_copy_pages(a, 16, 16, 0, 0) == want
-        assert m.kv_compact(a, *s, 16, 16, 1, 0) == want
-        assert m.kv_attention(a, 16, 1, 1, 16, 4, 4, 0, *s, 16, 2, 2, 0, 0, 0, 0, 1.0) == want
-    a = ctypes.addressof(good)
-    assert m.kv_append(a, 16, 1, 1, 16, 1, 1, *s, 16, 2, 9, 0) == 1      # dtype
-    assert m.kv_attention(a, 16, 1, 1, 16, 4, 4, 0, *s, 16, 2, 2, 5, 16, 0, 0, 1.0) == 2  # window and tree
-    for f, n in ((m.kv_append, 16), (m.kv_gather, 16), (m.kv_copy_pages, 5), (m.kv_compact, 10), (m.kv_attention, 21)):
-        with pytest.raises(TypeError):
-            f(*[0] * (n - 1))
-        with pytest.raises(TypeError):
-            f("a", *[0] * (n - 1))
-    with pytest.raises(TypeError):
-        m.kv_attention(*[0] * 20, "scale")
+    c = cache()
+    a, t = ctypes.addressof(c), torch.zeros(2, 2, 128, dtype=torch.float16)
+    for f, n in ((m.kv_append, 7), (m.kv_gather, 7), (m.kv_copy_pages, 4), (m.kv_compact, 6), (m.kv_attention, 11)):
+        for args in ([0] * (n - 1), [a, 0] + [t] * (n - 3), [a, 0] + [3] * (n - 2), ["a", 0] + [t] * (n - 2),
+                     [a, "0"] + [t] * (n - 2), [a, 0] + [None] * (n - 2)):
+            with pytest.raises(TypeError):
+                f(*args)
+        with pytest.raises(ValueError, match="CUDA device"):
+            f(a, 0, *[t] * (n - 2))
+        with pytest.raises(ValueError, match="null"):
+            f(0, 0, *[t] * (n - 2))
     with pytest.raises((ValueError, TypeError)):
-        m.bind_kv(0, 0, 0, 0, 0)
+        m.bind_kv(0, 0, 0, 0, 0, torch.Tensor)
+    with pytest.raises(TypeError):
+        m.bind_kv(1, 1, 1, 1, 1, 1)
 
 
 def test_cache_refuses_cpu_tensors():
