@@ -31,14 +31,11 @@
 // the resident blocks (qmm_kv_plan.h), whatever the lengths; a block's warps take them in turn, each
 // through its own cp.async ring.  Items that several blocks share are summed by the last of them to
 // arrive, in block order, so results do not depend on timing.
-#include <climits>
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>
 
-#include "qmm_common.cuh"
-#include "qmm_internal.h"
-#include "qmm_kv_plan.h"
+#include "qmm_attn.cuh"
 #include "sm100.cuh"
 
 namespace qmm_impl {
@@ -46,19 +43,6 @@ namespace {
 
 __device__ unsigned g_attn_errors;  // bit 1: a page or position outside the cache
 
-constexpr float kNoRef = -1e30f;  // reference of a query that has seen nothing yet
-constexpr unsigned kFull = 0xFFFFFFFFu;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
@@ -77,9 +61,6 @@ __device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ float half_lo(uint32_t v) { return __half2float(__ushort_as_half(uint16_t(v))); }
-__device__ __forceinline__ float half_hi(uint32_t v) { return __half2float(__ushort_as_half(uint16_t(v >> 16))); }
-
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
     float2 v;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
@@ -147,82 +128,6 @@ struct AttnFmt {
     static constexpr bool SUMS = NT == 1 && NG <= 4;       // V's codes centred by sums of P * s, not one by one
 };
 
-// Four values of an output row: sum / l, rounded once; with the first of them the row's lse.
-// A row that saw nothing (l = 0) is zeros and -infinity.
-__device__ __forceinline__ void store_row4(const AttnArgs& a, int row, int head, int d, float4 v, float l, float ref) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-    uint2 out;
-    if (a.is_bf16) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-        out = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    } else {
-        out = make_uint2(f32x2_to_f16x2(v.x, v.y), f32x2_to_f16x2(v.z, v.w));
-    }
-    *reinterpret_cast<uint2*>(a.o + int64_t(row) * a.o_ts + int64_t(head) * a.o_hs + d) = out;
-    if (d == 0 && a.lse != nullptr)
-        a.lse[int64_t(row) * (a.kv_heads * a.group_heads) + head] =
-            l == 0.f ? -INFINITY : (ref + lg2(l)) * 0.693147180559945309f;
-}
-
-__device__ __forceinline__ AttnSeq load_seq(const AttnArgs& a, int b, int rows) {
-    return attn_seq(a.cu[b], a.cu[b + 1], a.lens[b], a.tokens, a.capacity, a.group_heads, rows, a.window);
-}
-
-// Units and items of all sequences; false if offsets fall.
-__device__ __forceinline__ bool all_work(const AttnArgs& a, int rows, int lane, int* units, int* items) {
-    int u = 0, n = 0;
-    bool falls = false;
-    for (int b = lane; b < a.seqs; b += 32) {
-        const AttnSeq s = load_seq(a, b, rows);
-        falls |= s.falls;
-        u += attn_seq_units(s, a.kv_heads);
-        n += attn_seq_items(s, a.kv_heads);
-    }
-    *units = __reduce_add_sync(kFull, u);
-    *items = __reduce_add_sync(kFull, n);
-    return !__any_sync(kFull, falls);
-}
-
-// The sequence in which place x of the running sum of the sequences' weights falls (seqs if past the
-// end); *before = the sum of those in front of it.
-__device__ __forceinline__ int find_seq(const AttnArgs& a, const AttnPlan& p, int rows, int x, int lane, int* before) {
-    int base = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-        const int b = b0 + lane;
-        const int w = b < a.seqs ? attn_seq_weight(p, load_seq(a, b, rows), a.kv_heads) : 0;
-        int inc = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, inc, o);
-            if (lane >= o) inc += u;
-        }
-        const unsigned past = __ballot_sync(kFull, base + inc > x);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            *before = base + __shfl_sync(kFull, inc - w, l);
-            return b0 + l;
-        }
-        base += __shfl_sync(kFull, inc, 31);
-    }
-    return a.seqs;
-}
-
-// One block's share of one item.  Kept in shared memory, a copy a warp; it is looked at once an item.
-struct Run {
-    int row0, start, keys, units;  // of the sequence (AttnSeq)
-    int b, h;          // sequence, K/V head
-    int u0, n;         // first unit of the item, units
-    int row_lo, rows;  // first query row (of the sequence) and how many
-    int lo, hi;        // positions that some row sees
-    int full_lo, full_hi;  // positions [full_lo, full_hi) that every row sees
-    int t0;            // position of the first unit
-    int first;         // the item is the block's first
-    int c0, c1;        // the blocks that share the item
-    int x, before;     // place in the order of the blocks; weight of the sequences in front of b
-};
-static_assert(sizeof(Run) <= 96, "Run does not fit its place");
-
 template <int D, int GRP, int NT>
 __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(const __grid_constant__ AttnArgs a) {
     using F = AttnFmt<D, GRP, NT>;
@@ -235,53 +140,17 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
     grid_dependency_wait();
     grid_dependents_launch();
 
+    constexpr AttnCut cut{R, kAttnUnit, W};
     AttnPlan pl;
     int x_end;
-    Run* cur = reinterpret_cast<Run*>(smem + F::OFF_RUN + w * 192);
+    Run* cur = reinterpret_cast<Run*>(smem + F::OFF_RUN + w * 192);  // a copy a warp
     Run* next = cur + 1;
-
-    // ---- the item at place x of the order of the blocks, in or after sequence b, and this block's share
-    auto plan = [&](Run* r, int x, int b, int before, bool first_item) {
-        AttnSeq s = load_seq(a, b, R);
-        int weight = attn_seq_weight(pl, s, a.kv_heads);
-        while (x >= before + weight) {
-            before += weight;
-            s = load_seq(a, ++b, R);
-            weight = attn_seq_weight(pl, s, a.kv_heads);
-        }
-        const AttnShare sh = attn_share(pl, s, x, x_end, before);
-        const int h = sh.item / s.rt, row_lo = (sh.item - h * s.rt) * R, nrows = s.n * a.group_heads;
-        const int rows = nrows - row_lo < R ? nrows - row_lo : R;
-        const int first = s.start + row_lo / a.group_heads, last = s.start + (row_lo + rows - 1) / a.group_heads;
-        int lo, hi;
-        attn_range(s, row_lo, row_lo + rows, a.group_heads, a.window, a.tree != nullptr, &lo, &hi);
-        if (lane == 0) {
-            r->row0 = s.row0, r->start = s.start, r->keys = s.keys, r->units = s.units;
-            r->b = b, r->h = h, r->u0 = sh.u0, r->n = sh.n;
-            r->row_lo = row_lo, r->rows = rows, r->lo = lo, r->hi = hi;
-            const int all = a.tree ? s.start : first + 1;
-            r->full_hi = all < s.keys ? all : s.keys;
-            r->full_lo = a.window > 0 && last >= a.window ? last - a.window + 1 : 0;
-            r->t0 = s.lo + kAttnUnit * sh.u0;
-            r->first = first_item;
-            r->c0 = sh.c0, r->c1 = sh.c1, r->x = x, r->before = before;
-        }
-        __syncwarp();
-        return s.start + s.n > a.capacity;  // the table cannot name all of its positions
-    };
-    bool bad;
+    bool bad = false;
     {
-        int total, items, before = 0;
-        if (!all_work(a, R, lane, &total, &items)) {
-            if (blockIdx.x == 0 && tid == 0) atomicOr(&g_attn_errors, 2u);
-            return;
-        }
-        pl = attn_plan(total, items, gridDim.x, W);
-        const int x = pl.pieces ? int(blockIdx.x) : int(blockIdx.x) * pl.per;
-        x_end = pl.pieces ? x + 1 : x + pl.per < total ? x + pl.per : total;
-        const int b = find_seq(a, pl, R, x, lane, &before);
-        if (b >= a.seqs) return;
-        bad = plan(cur, x, b, before, true);
+        const int got = plan_block(a, cut, lane, lane == 0, &pl, &x_end, cur, &bad);
+        if (got < 0 && blockIdx.x == 0 && tid == 0) atomicOr(&g_attn_errors, 2u);
+        if (got <= 0) return;
+        __syncwarp();
     }
 
     // ---- tile copies.  Codes: 16-byte piece p of a tile goes to row p / CH, piece p % CH, xor-swizzled
@@ -735,7 +604,8 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
         const int x = pl.pieces ? x_end : cur->x + cur->n;
         const bool more = x < x_end;
         if (more) {
-            bad |= plan(next, x, cur->b, cur->before, false);
+            bad |= plan_run(a, pl, cut, x, x_end, cur->b, cur->before, false, lane == 0, next);
+            __syncwarp();
             q_first = load_q(next, tid);
             begin(next);
 #pragma unroll
@@ -770,10 +640,6 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
         __syncthreads();
         // ---- the block's sums: to the output, or to this block's slot of the workspace
         const bool whole = cur->n == cur->units;
-        auto put = [&](int row, int d, float4 sum, float lsum, float top) {
-            const int qr = cur->row_lo + row, tok = qr / a.group_heads;
-            store_row4(a, cur->row0 + tok, cur->h * a.group_heads + qr - tok * a.group_heads, d, sum, lsum, top);
-        };
         float* slot_o = a.part + int64_t(attn_slot(blockIdx.x, cur->first)) * F::SLOT;
         for (int i = tid; i < cur->rows * (D / 4); i += THREADS) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
@@ -795,57 +661,14 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                 lsum = fmaf(f, from[R * F::OROW + R + row], lsum);
             }
             if (whole) {
-                put(row, d, sum, lsum, top);
+                const int qr = cur->row_lo + row, tok = qr / a.group_heads;
+                store_row4(a, cur->row0 + tok, cur->h * a.group_heads + qr - tok * a.group_heads, d, sum, lsum, top);
             } else {
                 __stcg(reinterpret_cast<float4*>(slot_o + row * D + d), sum);
                 if (d == 0) __stcg(slot_o + R * D + row, top), __stcg(slot_o + R * D + R + row, lsum);
             }
         }
-        if (!whole) {
-            // the last of the item's blocks to arrive adds their sums in block order
-            const int c0 = cur->c0, c1 = cur->c1;
-            __threadfence();
-            __syncthreads();
-            int* flag = reinterpret_cast<int*>(smem + F::OFF_LAST);
-            if (tid == 0) *flag = atomicInc(a.count + c0, unsigned(c1 - c0)) == unsigned(c1 - c0);  // wraps to 0
-            __syncthreads();
-            if (*flag) {
-                __threadfence();
-                // the item is the first of its blocks, but for c0 where that began in front of it
-                const bool c0_first = pl.pieces || c0 * pl.per == cur->x - cur->u0;
-                auto slot_of = [&](int i) { return a.part + int64_t(attn_slot(i, i > c0 || c0_first)) * F::SLOT; };
-                for (int i = tid; i < cur->rows * (D / 4); i += THREADS) {
-                    const int row = i / (D / 4), d = i % (D / 4) * 4;
-                    float top = kNoRef, lsum = 0.f;
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q0 = c0; q0 <= c1; q0 += 8) {
-                        float4 v[8];
-                        float rf[8], ll[8], nt = top;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const bool on = q0 + k <= c1;
-                            const float* from = slot_of(on ? q0 + k : c1);
-                            rf[k] = on ? __ldcg(from + R * D + row) : kNoRef;
-                            ll[k] = on ? __ldcg(from + R * D + R + row) : 0.f;
-                            v[k] = on ? __ldcg(reinterpret_cast<const float4*>(from + row * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) nt = fmaxf(nt, rf[k]);
-                        const float f0 = ex2(top - nt);
-                        sum.x *= f0, sum.y *= f0, sum.z *= f0, sum.w *= f0, lsum *= f0;
-                        top = nt;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float f = ex2(rf[k] - top);
-                            sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
-                            sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
-                            lsum = fmaf(f, ll[k], lsum);
-                        }
-                    }
-                    put(row, d, sum, lsum, top);
-                }
-            }
-        }
+        if (!whole) join_item<D, R>(a, pl, cur, tid, THREADS, reinterpret_cast<int*>(smem + F::OFF_LAST));
         if (!more) break;
         __syncthreads();  // the sums' ring slots and Q are free
         Run* const was = cur;
@@ -869,8 +692,7 @@ AttnInst inst() {
 }
 template <int D, int GRP>
 AttnInst inst_nt(int nt) {
-    if constexpr (D == 256) return nt == 1 ? inst<D, GRP, 1>() : inst<D, GRP, 2>();
-    else return nt == 1 ? inst<D, GRP, 1>() : nt == 2 ? inst<D, GRP, 2>() : nt == 3 ? inst<D, GRP, 3>() : inst<D, GRP, 4>();
+    return nt == 1 ? inst<D, GRP, 1>() : inst<D, GRP, 2>();
 }
 AttnInst instance(int d, int grp, int nt) {
     if (d == 64) return grp == 32 ? inst_nt<64, 32>(nt) : inst_nt<64, 64>(nt);
@@ -878,24 +700,25 @@ AttnInst instance(int d, int grp, int nt) {
     return grp == 32 ? inst_nt<256, 32>(nt) : grp == 64 ? inst_nt<256, 64>(nt) : inst_nt<256, 128>(nt);
 }
 
-// SMs x resident blocks of an instance, once per device and instance.
-cudaError_t attn_resident(const AttnInst& k, int* out) {
+}  // namespace
+
+cudaError_t attn_resident(void (*fn)(const AttnArgs), int threads, int smem, int* out) {
     static std::mutex mu;
     static std::unordered_map<uint64_t, int> cache;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t key = reinterpret_cast<uint64_t>(k.fn) * 64 + uint64_t(dev);
+    const uint64_t key = reinterpret_cast<uint64_t>(fn) * 64 + uint64_t(dev);
     std::lock_guard<std::mutex> lk(mu);
     auto it = cache.find(key);
     if (it != cache.end()) {
         *out = it->second;
         return cudaSuccess;
     }
-    e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int per = 0, sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k.fn, k.threads, size_t(k.smem));
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, size_t(smem));
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -905,35 +728,24 @@ cudaError_t attn_resident(const AttnInst& k, int* out) {
     return cudaSuccess;
 }
 
-}  // namespace
-
-cudaError_t launch_attn(const AttnArgs& in, int head_dim, int group, cudaStream_t stream) {
-    AttnArgs a = in;
-    // query rows of a tile: the 8-row columns that the sequences' rows fill, so that the cache is
-    // streamed once wherever they fit.  Only the average is known here; where several sequences have
-    // several tokens, some are taken to have half as many again (columns that a tile does not fill
-    // cost next to nothing, but for the registers that more warps could have had)
-    const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
-    const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
-    const int64_t cols = (rows + 7) / 8, most = head_dim == 256 ? 2 : 4;
-    const AttnInst k = instance(head_dim, group, int(cols < most ? cols : most));
+cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threads, int smem, int slot, int rows, int unit,
+                               cudaStream_t stream) {
     int blocks = 0;
-    cudaError_t e = attn_resident(k, &blocks);
+    cudaError_t e = attn_resident(fn, threads, smem, &blocks);
     if (e != cudaSuccess) return e;
     // never more blocks than units there can be
-    const int64_t tiles = int64_t(a.tokens) * a.group_heads / k.rows + a.seqs;
-    const int64_t per_item = (int64_t(a.capacity) + kAttnUnit - 1) / kAttnUnit;
+    const int64_t tiles = int64_t(a.tokens) * a.group_heads / rows + a.seqs;
+    const int64_t per_item = (int64_t(a.capacity) + unit - 1) / unit;
     const int64_t units = tiles * a.kv_heads * (per_item > 0 ? per_item : 1);
     if (units >= int64_t(1) << 30) return cudaErrorNotSupported;
     if (units < blocks) blocks = int(units);
     if (blocks > kArrivalCounters) blocks = kArrivalCounters;
     void* ws = nullptr;
-    e = split_workspace(stream, size_t(2) * blocks * k.slot * sizeof(float), &ws);
+    e = split_workspace(stream, size_t(2) * blocks * slot * sizeof(float), &ws);
     if (e != cudaSuccess) return e;
     a.part = static_cast<float*>(ws);
     e = arrival_counters(stream, &a.count);
     if (e != cudaSuccess) return e;
-
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -942,9 +754,20 @@ cudaError_t launch_attn(const AttnArgs& in, int head_dim, int group, cudaStream_
     cfg.numAttrs = 1;
     cfg.stream = stream;
     cfg.gridDim = dim3(unsigned(blocks));
-    cfg.blockDim = dim3(unsigned(k.threads));
-    cfg.dynamicSmemBytes = size_t(k.smem);
-    return cudaLaunchKernelEx(&cfg, k.fn, static_cast<const AttnArgs>(a));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<const AttnArgs>(a));
+}
+
+cudaError_t launch_attn(const AttnArgs& a, int head_dim, int group, cudaStream_t stream) {
+    // query rows of a tile: what the sequences have, so that the cache is streamed once wherever they
+    // fit.  Only the average is known here; where several sequences have several tokens, some are
+    // taken to have half as many again (columns that a tile does not fill cost next to nothing)
+    const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
+    const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
+    if (rows > 8 && attn_tc_supported(head_dim)) return launch_attn_tc(a, head_dim, group, rows, stream);
+    const AttnInst k = instance(head_dim, group, rows <= 8 ? 1 : 2);
+    return launch_attn_blocks(a, k.fn, k.threads, k.smem, k.slot, k.rows, kAttnUnit, stream);
 }
 
 cudaError_t attn_read_and_clear_errors(unsigned* out) {
@@ -952,7 +775,10 @@ cudaError_t attn_read_and_clear_errors(unsigned* out) {
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_errors, sizeof(v));
     if (e != cudaSuccess) return e;
     e = cudaMemcpyToSymbol(g_attn_errors, &zero, sizeof(zero));
-    *out = v;
+    if (e != cudaSuccess) return e;
+    unsigned t = 0;
+    e = attn_tc_read_and_clear_errors(&t);
+    *out = v | t;
     return e;
 }
 

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int b = seq_of(a.cu, a.seqs, w.tok);
     int64_t at = -1;
     if (w.on && b < a.seqs && a.cu[b] <= w.tok) {  // rows in front of the first or behind the last sequence are left
-        const AttnSeq s = attn_seq(a.cu[b], a.cu[b + 1], a.at[b], a.tokens, a.capacity, 1, 1, 0);
+        const AttnSeq s = attn_seq(a.cu[b], a.cu[b + 1], a.at[b], a.tokens, a.capacity, 1, 1, kAttnUnit, 0);
         at = cache_row(a, b, s.start + (w.tok - s.row0), w.h);
         flag_bad(at < 0);
     }

@@ -14,7 +14,8 @@
 namespace qmm_impl {
 
 constexpr int kAttnSub = 16;              // positions whose page is looked up once (pages are multiples of it)
-constexpr int kAttnUnit = 2 * kAttnSub;   // positions a warp takes at a time: attention's unit of work
+constexpr int kAttnUnit = 2 * kAttnSub;   // unit of work of the warps' kernel: what a warp takes at a time
+constexpr int kAttnTcUnit = 128;          // unit of work of the tensor-core kernel: what a block takes at a time
 
 // One sequence of an attention call.
 struct AttnSeq {
@@ -32,7 +33,8 @@ QMM_HD int clamp_int(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi :
 
 // c0, c1: the sequence's entries of the offsets; every value is taken as it comes from device
 // memory, so nothing derived from them may leave [0, tokens] and [0, capacity].
-QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int group_heads, int rows, int window) {
+QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int group_heads, int rows, int unit,
+                         int window) {
     AttnSeq s;
     s.row0 = clamp_int(c0, 0, tokens);
     s.n = clamp_int(c1, 0, tokens) - s.row0;
@@ -47,7 +49,7 @@ QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int g
         if (s.lo > s.keys) s.lo = s.keys;
         s.lo -= s.lo % kAttnSub;
     }
-    s.units = (s.keys - s.lo + kAttnUnit - 1) / kAttnUnit;
+    s.units = (s.keys - s.lo + unit - 1) / unit;
     if (s.units < 1) s.units = 1;
     s.rt = int((int64_t(s.n) * group_heads + rows - 1) / rows);
     return s;
@@ -63,15 +65,15 @@ QMM_HD int ceil_div_int(int a, int b) { return (a - 1) / b + 1; }  // a >= 1
 
 // How the work is dealt out over `blocks` blocks.  Even shares: block i takes units [i * per,
 // (i + 1) * per) of all, across items; a block whose share holds the end of one item and the start of
-// the next changes items, which costs about as much as kAttnChange units.  Pieces, where items are
+// the next changes items, which costs about as much as kAttnChange positions.  Pieces, where items are
 // few: each item is cut into pieces of `per` units (the last one shorter), one a block, so that no
 // block changes items; the pieces are as small as keeps their number within the blocks, and give each
 // of a block's warps a unit at least.
-constexpr int kAttnChange = 12;
+constexpr int kAttnChange = 384;
 struct AttnPlan {
     int total, per, pieces;  // units of all; units a block; 1: pieces
 };
-QMM_HD AttnPlan attn_plan(int total, int items, int blocks, int warps) {
+QMM_HD AttnPlan attn_plan(int total, int items, int blocks, int unit, int warps) {
     AttnPlan p;
     p.total = total;
     p.pieces = 0;
@@ -79,7 +81,7 @@ QMM_HD AttnPlan attn_plan(int total, int items, int blocks, int warps) {
     if (total > 0 && items < blocks) {
         int piece = ceil_div_int(total, blocks - items);
         if (piece < warps) piece = warps;
-        if (piece <= p.per + kAttnChange) p.pieces = 1, p.per = piece;
+        if (piece <= p.per + kAttnChange / unit) p.pieces = 1, p.per = piece;
     }
     return p;
 }

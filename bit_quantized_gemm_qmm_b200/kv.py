@@ -110,8 +110,8 @@ def kv_gather(cache: KVCache, page_table: torch.Tensor, starts: torch.Tensor, cu
     """Cache rows as dense (k, v) [tokens, kv_heads, head_dim]: rows cu_tokens[b] + i are positions
     starts[b] + i of sequence b.  Rows of no sequence are left as they are."""
     if out is None:
-        both = torch.empty((2, tokens, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
-        k, v = both[0], both[1]
+        k = torch.empty(tokens, cache.kv_heads, cache.head_dim, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         if k.shape[0] != tokens or k.dtype is not dtype:
@@ -141,11 +141,11 @@ def kv_attention(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lens
     `window` positions up to its own.  tree: int64 [tokens], bit j of a token's mask set where it sees
     its sequence's new token j (and every position before the new ones).  o has q's dtype; lse is fp32
     [tokens, heads], -inf where a row sees nothing.  Rows of no sequence are left as they are."""
-    shape = q.shape
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=cache.device)
+        n, heads = q.shape[:2]
+        lse = torch.empty(n, heads, dtype=torch.float32, device=cache.device)
     _run(cache, _calls().kv_attention, q, page_table, lens, cu_tokens, out, lse, tree, window,
          cache.scale if scale is None else scale)
     return out, lse

@@ -32,6 +32,13 @@ def rows_of(arrays, table_row, positions, page):
     return out
 
 
+def many_rows(q, hk, seqs):
+    """Whether the tensor-core kernel takes the call (launch_attn's rule)."""
+    mean = -(-q.shape[0] // seqs)
+    rows = (mean + mean // 2 if seqs > 1 else mean) * (q.shape[1] // hk)
+    return rows > 8 and q.shape[2] <= 128
+
+
 def attention(arrays, page, q, table, lens, cu, scale, window=0, tree=None):
     """(o, lse, o's bound, lse's bound) in 64 bits; rows of no sequence are NaN.
 
@@ -40,7 +47,12 @@ def attention(arrays, page, q, table, lens, cu, scale, window=0, tree=None):
     twice that in relative terms (their own and the sum's) plus 2^-20 for exp2 and the fp32 sums.
     P * s is rounded to fp16 (2^-11 of it, times |code - 8|); below 2^-14 of the fp16 range it is
     subnormal, where the error is 2^-25 in units in which the row's largest P * s is 2^-4 at least,
-    so 2^-18 of the largest P * s for each such position.  The result is rounded once."""
+    so 2^-18 of the largest P * s for each such position.  The result is rounded once.
+
+    The kernel for many rows rounds V to fp16 instead (2^-11 |v|; a subnormal one by 2^-25), and P: once for bf16
+    (2^-11, below 2^-14 by 2^-25 where the row's largest P is 1 at least), in two terms for fp16 (2^-22,
+    covered by the score's share; the same below 2^-14)."""
+    many = many_rows(q, arrays[0].shape[1], len(lens))
     T, H, D = q.shape
     hk = arrays[0].shape[1]
     grp = H // hk
@@ -85,5 +97,10 @@ def attention(arrays, page, q, table, lens, cu, scale, window=0, tree=None):
                 low = (ps < top[:, None] * 2.0 ** -10).sum(1)
                 ob[r0 + i, hs] = (2 * dx + 2.0 ** -20) * (w @ (vs[h, idx] * vc[h, idx] + vb[h, idx].abs() + 8 * vs[h, idx])) \
                     + 2.0 ** -11 * (w @ (vs[h, idx] * (vc[h, idx] - 8).abs())) + low * 2.0 ** -18 * top
+                if many:
+                    av = vv.abs()
+                    wv = w @ av
+                    ob[r0 + i, hs] = (2 * dx + 2.0 ** -20) * wv + 2.0 ** -11 * wv * (2 + 2.0 ** -10 if q.dtype == torch.bfloat16 else 1) \
+                        + 2.0 ** -25 + idx.numel() * 2.0 ** -25 * w.amax(-1, keepdim=True) * av.amax(0)
                 lb[r0 + i, hs] = dx.flatten() + 2.0 ** -21 * lse[r0 + i, hs].abs() + 2.0 ** -20
     return o, lse, ob + SIXTEEN[q.dtype] * (o.abs() + ob), lb

@@ -19,13 +19,13 @@ HARNESS = r"""
 using namespace qmm_impl;
 // Walks the blocks as the kernels do.  Returns 0, or the number of the first check that fails.
 extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int capacity, int kv_heads, int gh, int rows,
-                    int window, int tree, int blocks, int warps) {
+                    int window, int tree, int blocks, int unit, int warps) {
     std::vector<AttnSeq> s;
     std::vector<int> item0, unit0;  // items and units in front of each sequence
     int total = 0, items = 0;
     for (int b = 0; b < seqs; ++b) {
         if (cu[b + 1] < cu[b]) return 0;  // nothing is done
-        s.push_back(attn_seq(cu[b], cu[b + 1], lens[b], tokens, capacity, gh, rows, window));
+        s.push_back(attn_seq(cu[b], cu[b + 1], lens[b], tokens, capacity, gh, rows, unit, window));
         const AttnSeq& q = s.back();
         if (q.row0 < 0 || q.n < 0 || q.row0 + q.n > tokens || q.keys < 0 || q.keys > capacity) return 1;
         if (q.lo < 0 || q.lo % kAttnSub || q.lo > q.keys || q.units < 1) return 2;
@@ -33,7 +33,7 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
         total += attn_seq_units(q, kv_heads);
         items += attn_seq_items(q, kv_heads);
     }
-    const AttnPlan p = attn_plan(total, items, blocks, warps);
+    const AttnPlan p = attn_plan(total, items, blocks, unit, warps);
     if (p.per < 1) return 3;
     std::vector<int> taken(total, 0), slots(2 * blocks, -1);  // slot -> item
     struct Shared { int c0, c1, first; };
@@ -72,9 +72,9 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
             attn_range(s[b], r0, r0 + nr, gh, window, tree, &lo, &hi);
             if (lo < 0 || hi < 0 || hi > s[b].keys) return 13;
             if (window > 0 && lo < s[b].lo) return 14;
-            const int t0 = s[b].lo + kAttnUnit * h.u0;
+            const int t0 = s[b].lo + unit * h.u0;
             std::vector<int> by(h.n, 0);  // units some warp takes
-            for (int w = 0; w < warps; ++w) {
+            for (int w = 0; unit == kAttnUnit && w < warps; ++w) {
                 int j0, j1;
                 attn_warp_units(t0, h.n, w, warps, lo, hi, &j0, &j1);
                 if (j0 < 0) return 15;
@@ -84,9 +84,9 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
                 }
             }
             for (int u = 0; u < h.n; ++u) {
-                const int t = t0 + kAttnUnit * u;
-                const bool any = t < hi && t + kAttnUnit > lo && t < s[b].keys;
-                if (by[u] != (any ? 1 : 0)) return 17;
+                const int t = t0 + unit * u;
+                const bool any = t < hi && t + unit > lo && t < s[b].keys;
+                if (unit == kAttnUnit && by[u] != (any ? 1 : 0)) return 17;
                 if (t < 0 || t % kAttnSub) return 18;
             }
             x = p.pieces ? end : x + h.n;
@@ -138,7 +138,7 @@ def test_every_unit_once_and_every_slot_its_own(walk):
         tree = 0 if window else rng.choice([0, 1])
         arr = lambda v: (ctypes.c_int * len(v))(*v)  # noqa: E731
         args = (seqs, arr(cu), arr(lens), tokens, page_cap, rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 8]),
-                rng.choice([8, 16, 24, 32]), window, tree, rng.choice([1, 2, 7, 148, 296]), rng.choice([4, 6]))
+                rng.choice([8, 16, 32, 64]), window, tree, rng.choice([1, 2, 7, 148, 296]), *rng.choice([(32, 4), (32, 6), (128, 1)]))
         got = walk(*args)
         assert got == 0, (got, seqs, cu, lens, args[3:])
 
