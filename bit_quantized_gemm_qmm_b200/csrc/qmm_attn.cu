@@ -702,7 +702,7 @@ AttnInst instance(int d, int grp, int nt) {
 
 }  // namespace
 
-cudaError_t attn_resident(void (*fn)(const AttnArgs), int threads, int smem, int* out) {
+cudaError_t attn_blocks(void (*fn)(const AttnArgs), int smem, int per_sm, int regs, int* out) {
     static std::mutex mu;
     static std::unordered_map<uint64_t, int> cache;
     int dev = 0;
@@ -717,21 +717,24 @@ cudaError_t attn_resident(void (*fn)(const AttnArgs), int threads, int smem, int
     }
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int per = 0, sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, size_t(smem));
-    if (e != cudaSuccess) return e;
+    if (regs) {
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, fn);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != regs) return cudaErrorInvalidConfiguration;
+    }
+    int sms = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (per < 1) return cudaErrorInvalidConfiguration;
-    *out = per * sms;
+    *out = per_sm * sms;
     cache.emplace(key, *out);
     return cudaSuccess;
 }
 
 cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threads, int smem, int slot, int rows, int unit,
-                               cudaStream_t stream) {
+                               int regs, cudaStream_t stream) {
     int blocks = 0;
-    cudaError_t e = attn_resident(fn, threads, smem, &blocks);
+    cudaError_t e = attn_blocks(fn, smem, 2, regs, &blocks);  // both kernels are built for two blocks an SM
     if (e != cudaSuccess) return e;
     // never more blocks than units there can be
     const int64_t tiles = int64_t(a.tokens) * a.group_heads / rows + a.seqs;
@@ -767,7 +770,7 @@ cudaError_t launch_attn(const AttnArgs& a, int head_dim, int group, cudaStream_t
     const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
     if (rows > 8 && attn_tc_supported(head_dim)) return launch_attn_tc(a, head_dim, group, rows, stream);
     const AttnInst k = instance(head_dim, group, rows <= 8 ? 1 : 2);
-    return launch_attn_blocks(a, k.fn, k.threads, k.smem, k.slot, k.rows, kAttnUnit, stream);
+    return launch_attn_blocks(a, k.fn, k.threads, k.smem, k.slot, k.rows, kAttnUnit, 0, stream);
 }
 
 cudaError_t attn_read_and_clear_errors(unsigned* out) {

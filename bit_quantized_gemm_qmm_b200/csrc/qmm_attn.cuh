@@ -202,11 +202,12 @@ __device__ __forceinline__ void join_item(const AttnArgs& a, const AttnPlan& pl,
     }
 }
 
-// Blocks of a kernel that the device holds at once, once per device and kernel.
-cudaError_t attn_resident(void (*fn)(const AttnArgs), int threads, int smem, int* out);
+// per_sm blocks for each of the device's SMs; allows the kernel its shared memory, once per device and kernel.
+// regs: registers a thread that the kernel must have been built with (it shares them out anew), or 0.
+cudaError_t attn_blocks(void (*fn)(const AttnArgs), int smem, int per_sm, int regs, int* out);
 // Launches a kernel over the resident blocks, with its workspace.
 cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threads, int smem, int slot, int rows, int unit,
-                               cudaStream_t stream);
+                               int regs, cudaStream_t stream);
 // The tensor-core kernel (qmm_attn_tc.cu); rows: query rows of the longer sequences.
 bool attn_tc_supported(int head_dim);
 cudaError_t launch_attn_tc(const AttnArgs& a, int head_dim, int group, int64_t rows, cudaStream_t stream);

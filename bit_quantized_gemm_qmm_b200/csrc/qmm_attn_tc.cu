@@ -2,23 +2,23 @@
 //
 // The same operation as qmm_attn.cu, for tiles of up to 64 query rows against 128 positions at a
 // time: drafts of several tokens, chunks of a prompt.  Positions are the MMA's 128 rows and query rows
-// its columns, so that each of the block's 128 threads owns one position: what belongs to a position
-// (page, codes, scales, validity) is its thread's own, and few query rows still give every thread work.
+// its columns, so that what belongs to a position (page, codes, scales, validity) is one thread's own, and
+// few query rows still give every thread work.  One warpgroup converts, one does the softmax:
 //
-//   1. K: the thread writes its row's codes to shared memory as fp16 (a nibble in place is the
+//   1. K: a converting thread writes its row's codes to shared memory as fp16 (a nibble in place is the
 //      subnormal q * 2^-24, one place up q * 2^-20; the factor 16 is in Q), and its biases as 16 more
 //      columns against three fp16 terms of each group's sum of Q.  tcgen05.mma sums each group into
 //      columns of its own in tensor memory, and the biases into more.
-//   2. V: while that runs, the row as RN_fp16(s q + b) (what qmm_dequantize gives).
-//   3. The thread reads its position's sums: x = f * (bias + sum over groups of s * sum) - ref, all
+//   2. V: the row as RN_fp16(s q + b) (what qmm_dequantize gives).
+//   3. A softmax thread reads its position's sums: x = f * (bias + sum over groups of s * sum) - ref, all
 //      fp32, P = 2^x, and keeps its share of the rows' sums l in registers; P goes to shared memory as
 //      fp16 (for fp16 outputs as two terms, so that V's rounding is the only one before the output's).
 //   4. O^T += V^T P: V's rows as they are stored are the transposed (MN-major) operand, and so is P.
 //
 // References are moved only when some x passes 14 (fp16 holds P up to 2^15): then by the largest x of
-// the tile (redux over the warps' lanes), with O rescaled in tensor memory.  K and P share their
-// shared memory (K is read before P is written).  Two blocks an SM, so that one block's
-// conversions run beside the other's MMAs; the raw rows of the next tile are loaded ahead into registers.
+// the tile (redux over the warps' lanes), with O rescaled in tensor memory.  K of the next tile is converted and
+// its scores are under way while this tile's softmax runs; two blocks an SM fill what waits are left.
+// Every wait on a barrier is bounded; a block whose wait runs out goes through its barriers and says so.
 // Work and joins are those of qmm_attn.cu, in units of 128 positions.
 #include <climits>
 
@@ -32,28 +32,36 @@ using namespace sm100;
 
 __device__ unsigned g_tc_attn_errors;  // bit 0: a wait ran out; bit 1: a page or position outside the cache
 
-constexpr int kPos = kAttnTcUnit;  // positions a tile, and threads a block
+constexpr int kPos = kAttnTcUnit;          // positions a tile
+constexpr int kTcThreads = 2 * kPos;       // a warpgroup for the softmax, one for the conversions
 constexpr float kMaxX = 14.f;
+constexpr int kRegsS = 152, kRegsC = 104;  // registers a thread of the two, of 128 each at the launch: their sum is 256
 
 template <int D, int GRP, int N>
 struct TcAttnFmt {
     static constexpr int NG = D / GRP;
     static constexpr int WORDS = D / 8;                // 32-bit words of codes a row: 16-byte pieces as fp16
+    static constexpr int CH = 8;                       // query rows read from tensor memory at a time
+    // whether the two warpgroups share their registers out anew
+    static constexpr bool SPLIT = N > 32;
     static constexpr int PANELS = D / 64;              // 128-byte wide panels of a row of D fp16
     static constexpr int PANEL = kPos * 128;           // bytes of a panel of K or V
     // V first: where D = 64, V's MMA reads a second panel behind it, whose rows of O^T nobody looks at
     static constexpr int OFF_V = 0;
-    static constexpr int OFF_K = PANELS * PANEL;       // K, then P (two terms)
-    static constexpr int OFF_KB = OFF_K + 2 * PANEL;   // biases: 16 columns, [2][kPos] 16-byte pieces
-    static constexpr int OFF_Q = OFF_KB + kPos * 32;
+    static constexpr int OFF_K = PANELS * PANEL;
+    static constexpr int OFF_P = 2 * PANELS * PANEL;   // P; with N <= 32 its second term in the rows' other halves
+    static constexpr int OFF_Q = OFF_P + PANEL;
     static constexpr int QPANEL = N * 128;
-    static constexpr int OFF_QB = OFF_Q + PANELS * QPANEL;
-    static constexpr int OFF_F = OFF_QB + N * 32;      // per row: factor of the sums, reference
+    static constexpr int OFF_KB = OFF_Q + PANELS * QPANEL;  // biases: 16 columns, [2][kPos] 16-byte pieces
+    static constexpr int OFF_QB = OFF_KB + kPos * 32;
+    static constexpr int OFF_F = OFF_QB + N * 32;      // per row: factor of the sums; minus the reference
+    static constexpr int OFF_NREF = OFF_F + N * 4;
     static constexpr int OFF_LIM = OFF_F + N * 8;
     static constexpr int OFF_BITS = OFF_LIM + N * 4;
     static constexpr int OFF_RED = OFF_BITS + N * 8;   // per warp and row
-    static constexpr int OFF_BAR = OFF_RED + 4 * N * 4;
-    static constexpr int OFF_RUN = OFF_BAR + 32;       // this run and the next
+    static constexpr int OFF_POS = OFF_RED + 4 * N * 4;    // per position, for two tiles: K's scales, what is the matter
+    static constexpr int OFF_BAR = OFF_POS + 2 * kPos * (NG + 1) * 4;
+    static constexpr int OFF_RUN = OFF_BAR + 64;       // this run and the next
     static constexpr int USED = OFF_RUN + 2 * 96;
     static constexpr int SMEM = (USED > 80 * 1024 ? USED : 80 * 1024) + 1024;  // two blocks an SM at most; alignment
     // tensor memory columns: group sums, biases, O^T
@@ -74,14 +82,59 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr)
-        : "memory");
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) { tmem_ld_32x32b_x8(taddr, v); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) { tmem_st_32x32b_x8(taddr, v); }
+// Pairs of fp32 in one register pair: two results an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
 }
+__device__ __forceinline__ uint64_t bits2(uint32_t a, uint32_t b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Barriers of one warpgroup (1: conversions, 2: softmax).
+__device__ __forceinline__ void group_sync(int id) {
+    __syncwarp();
+    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool group_or(int id, bool v) {
+    uint32_t r;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred.aligned q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(uint32_t(v))
+        : "memory");
+    return r != 0;
+}
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ float warp_max(float v) {
     float r;
@@ -89,17 +142,24 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
+// What is the matter with a position (OFF_POS): it is not there; its V is not finite.
+constexpr uint32_t kAbsent = 1, kOdd = 2;
+
 template <int D, int GRP, int N>
-__global__ void __launch_bounds__(kPos, 2) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
     using F = TcAttnFmt<D, GRP, N>;
-    constexpr int NG = F::NG, WORDS = F::WORDS;
+    constexpr int NG = F::NG, WORDS = F::WORDS, CH = F::CH, HR = N > 32 ? 32 : N;
     extern __shared__ uint8_t raw_smem[];
     uint8_t* const smem = raw_smem + (1024 - (smem_addr(raw_smem) & 1023)) % 1024;  // swizzle atoms
     const uint32_t sbase = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const uint32_t bar_s = sbase + F::OFF_BAR, bar_o = bar_s + 8;
-    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + F::OFF_BAR + 16);
-    int* const flag = reinterpret_cast<int*>(smem + F::OFF_BAR + 20);
+    const int me = tid & (kPos - 1);     // this thread's position of a tile
+    const bool softmax = tid < kPos;
+    // full: scores of a tile are in tensor memory, K's place is free, and OFF_POS is written; free: the scores
+    // have been read; vfull: V is in place; done: O is up to date, V's and P's places are free
+    const uint32_t bar_full = sbase + F::OFF_BAR, bar_free = bar_full + 8, bar_vfull = bar_full + 16, bar_done = bar_full + 24;
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + F::OFF_BAR + 32);
+    int* const flag = reinterpret_cast<int*>(smem + F::OFF_BAR + 36);
 
     grid_dependency_wait();
 
@@ -115,8 +175,10 @@ __global__ void __launch_bounds__(kPos, 2) attn_tc_kernel(const __grid_constant_
         if (got <= 0) return;
     }
     if (tid == 0) {
-        mbar_init(bar_s, 1);
-        mbar_init(bar_o, 1);
+        mbar_init(bar_full, kPos + 1);
+        mbar_init(bar_free, kPos);
+        mbar_init(bar_vfull, kPos);
+        mbar_init(bar_done, 1);
         fence_mbar_init();
     }
     if (w == 0) {
@@ -124,62 +186,43 @@ __global__ void __launch_bounds__(kPos, 2) attn_tc_kernel(const __grid_constant_
         tmem_relinquish();
     }
     // columns of the bias operands that no group uses are zeros
-    for (int i = tid; i < kPos * 8; i += kPos) reinterpret_cast<uint32_t*>(smem + F::OFF_KB)[i] = 0;
-    for (int i = tid; i < N * 8; i += kPos) reinterpret_cast<uint32_t*>(smem + F::OFF_QB)[i] = 0;
+    for (int i = tid; i < kPos * 8; i += kTcThreads) reinterpret_cast<uint32_t*>(smem + F::OFF_KB)[i] = 0;
+    for (int i = tid; i < N * 8; i += kTcThreads) reinterpret_cast<uint32_t*>(smem + F::OFF_QB)[i] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     // only now: a following kernel's blocks may take tensor memory as soon as they are resident
     grid_dependents_launch();
     const uint32_t tmem = *tmem_at;
-    const uint32_t tmem_row = tmem + (uint32_t(w * 32) << 16);  // this warp's lanes
+    const uint32_t tmem_row = tmem + (uint32_t((w & 3) * 32) << 16);  // this warp's lanes
     constexpr uint32_t idesc = idesc_f16_f32(128, N);
     constexpr uint32_t idesc_t = idesc | 1u << 15 | 1u << 16;   // both operands MN-major
-    uint32_t par_s = 0, par_o = 0;
+    uint32_t tile = 0;  // tiles so far: the barriers' phases
     bool dead = false;
-    auto wait = [&](uint32_t bar, uint32_t& parity) {
-        if (!dead && !mbar_wait(bar, parity, clock64() + 4000000000ll)) dead = true;  // about two seconds
-        parity ^= 1;
-    };
-
-    // ---- this thread's position of the next tile: raw rows in registers
-    uint4 kr[WORDS / 4], vr[WORDS / 4];
-    uint16_t ksr[NG], kbr[NG], vsr[NG], vbr[NG];
-    bool there = false;
-    auto fetch = [&](const Run* r, int u) {  // unit u of the run
-        const int t = r->t0 + kPos * u + tid;
-        there = false;
-        if (u < r->n && t < r->hi && t >= 0) {
-            const int col = t / a.page, page = a.table[int64_t(r->b) * a.table_stride + col];
-            there = page >= 0 && page < a.pages;
-            bad |= !there;
-            if (there) {
-                const int64_t row = (int64_t(page) * a.kv_heads + r->h) * a.page + (t - col * a.page);
-                const uint4* k = reinterpret_cast<const uint4*>(a.kc + row * (D / 2));
-                const uint4* v = reinterpret_cast<const uint4*>(a.vc + row * (D / 2));
-#pragma unroll
-                for (int i = 0; i < WORDS / 4; ++i) kr[i] = __ldg(k + i), vr[i] = __ldg(v + i);
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    ksr[j] = __ldg(a.ks + row * NG + j), kbr[j] = __ldg(a.kb + row * NG + j);
-                    vsr[j] = __ldg(a.vs + row * NG + j), vbr[j] = __ldg(a.vb + row * NG + j);
-                }
+    auto wait = [&](uint32_t bar, uint32_t of) {  // until tile number `of` of the block has passed
+        if (dead || mbar_try_wait(bar, of & 1)) return;
+        const long long deadline = clock64() + 4000000000ll;  // about two seconds
+        while (!mbar_try_wait(bar, of & 1))
+            if (clock64() > deadline) {
+                dead = true;
+                break;
             }
-        }
     };
     // first unit at or behind u that some row sees a position of; n if none
     auto seek = [&](const Run* r, int u) {
         if (r->lo > r->t0 + kPos * (u + 1) - 1) u = (r->lo - r->t0) / kPos;
-        return r->t0 + kPos * u < r->hi ? u : r->n;
+        return r->t0 + kPos * u < r->hi && u < r->n ? u : r->n;
     };
     // panel-swizzled place of 16-byte piece p of row r
     auto place = [](int row, int p, int panel_bytes) { return (p >> 3) * panel_bytes + row * 128 + (((p & 7) ^ (row & 7)) << 4); };
+    uint32_t own[8];  // 16-byte pieces of this thread's position
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] = sbase + place(me, i, 0);
+    auto put = [&](int off, int p, uint4 v) { sts_v4(own[p & 7] + off + (p >> 3) * F::PANEL, v); };
 
-    int u = seek(cur, 0);
-    fetch(cur, u);
-    while (true) {
-        // ---- Q: K-major panels, scaled by a power of two per row (as in qmm_attn.cu)
-        for (int i = tid; i < N * WORDS; i += kPos) {
+    // ---- Q of the current run: K-major panels, scaled by a power of two per row (as in qmm_attn.cu)
+    auto stage_q = [&]() {
+        for (int i = tid; i < N * WORDS; i += kTcThreads) {
             const int row = i / WORDS, p8 = i % WORDS;
             const int qr = cur->row_lo + row, tok = qr / a.group_heads, hg = qr - tok * a.group_heads;
             uint32_t rw[4] = {0, 0, 0, 0};
@@ -230,267 +273,377 @@ __global__ void __launch_bounds__(kPos, 2) attn_tc_kernel(const __grid_constant_
                 }
             }
             if (p8 == 0) {
-                *reinterpret_cast<float2*>(smem + F::OFF_F + row * 8) = make_float2(a.scale_log2 * 16777216.f * exp2i(-e), kNoRef);
+                *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * 16777216.f * exp2i(-e);
+                *reinterpret_cast<float*>(smem + F::OFF_NREF + row * 4) = -kNoRef;
                 *reinterpret_cast<int*>(smem + F::OFF_LIM + row * 4) = row < cur->rows ? cur->start + tok : INT_MAX;
                 *reinterpret_cast<int64_t*>(smem + F::OFF_BITS + row * 8) =
                     a.tree != nullptr && row < cur->rows ? a.tree[cur->row0 + tok] : -1;
             }
         }
-        float l[N];
-#pragma unroll
-        for (int r = 0; r < N; ++r) l[r] = 0.f;
-        bool any_tile = false;
+        fence_async_smem();
+    };
 
-        while (u < cur->n) {
-            const int t = cur->t0 + kPos * u + tid;
-            const bool mine = there;
-            const bool masked = !(cur->t0 + kPos * u >= cur->full_lo && cur->t0 + kPos * (u + 1) <= cur->full_hi);
-            float ks[NG];
-            // ---- K to shared memory (P of the last tile was there)
-            if (any_tile) wait(bar_o, par_o);
+    if (!softmax) {
+        // ================================================= conversions: K and V of a position a thread
+        if constexpr (F::SPLIT) regs_down<kRegsC>();
+        uint4 kr[WORDS / 4], vr[WORDS / 4];
+        uint16_t ksr[NG], kbr[NG], vsr[NG], vbr[NG];
+        int page = -1;
+        int64_t row = -1;  // of the cache, for the tile that is fetched; -1: not there
+        auto look = [&](const Run* r, int u) {  // the page, a tile ahead of the rows
+            const int t = r->t0 + kPos * u + me;
+            page = u < r->n && t < r->hi ? a.table[int64_t(r->b) * a.table_stride + t / a.page] : -1;
+        };
+        auto fetch_k = [&](const Run* r, int u) {
+            const int t = r->t0 + kPos * u + me;
+            const bool in = u < r->n && t < r->hi, there = in && page >= 0 && page < a.pages;
+            bad |= in && !there;
+            row = there ? (int64_t(page) * a.kv_heads + r->h) * a.page + t % a.page : -1;
+            if (there) {
+                const uint4* k = reinterpret_cast<const uint4*>(a.kc + row * (D / 2));
 #pragma unroll
-            for (int j = 0; j < NG; ++j) ks[j] = __half2float(__ushort_as_half(ksr[j]));
+                for (int i = 0; i < WORDS / 4; ++i) kr[i] = __ldg(k + i);
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) {
-                const uint4 q = kr[i >> 2];
-                const uint32_t c = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w, y = c >> 8;
-                sts_v4(sbase + F::OFF_K + place(tid, i, F::PANEL),
-                       make_uint4(c & 0x000F000Fu, c & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u));
-            }
-#pragma unroll
-            for (int j = 0; j < NG; ++j)
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const int c = 3 * j + k;
-                    *reinterpret_cast<uint16_t*>(smem + F::OFF_KB + (c >> 3) * (kPos * 16) + tid * 16 + (c & 7) * 2) = mine ? kbr[j] : 0;
+                for (int j = 0; j < NG; ++j) {
+                    ksr[j] = __ldg(a.ks + row * NG + j), kbr[j] = __ldg(a.kb + row * NG + j);
+                    vsr[j] = __ldg(a.vs + row * NG + j), vbr[j] = __ldg(a.vb + row * NG + j);
                 }
-            fence_async_smem();
-            tc_fence_before();
+            }
+        };
+        auto fetch_v = [&]() {  // of the row that fetch_k found
+            if (row >= 0) {
+                const uint4* v = reinterpret_cast<const uint4*>(a.vc + row * (D / 2));
+#pragma unroll
+                for (int i = 0; i < WORDS / 4; ++i) vr[i] = __ldg(v + i);
+            }
+        };
+        int u = seek(cur, 0);
+        look(cur, u);
+        fetch_k(cur, u);
+        fetch_v();
+        look(cur, seek(cur, u + 1));
+        while (true) {
+            stage_q();
             __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
+            while (u < cur->n) {
+                const bool there = row >= 0;
+                const bool masked = !(cur->t0 + kPos * u >= cur->full_lo && cur->t0 + kPos * (u + 1) <= cur->full_hi);
+                const int u_next = seek(cur, u + 1);
+                bool odd = false;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t o = (k & 3) * 32;
-                    umma_f16_ss(tmem + (k * 16 / GRP) * N, smem_desc_sw128(sbase + F::OFF_K + (k >> 2) * F::PANEL + o, 1024),
-                                smem_desc_sw128(sbase + F::OFF_Q + (k >> 2) * F::QPANEL + o, 1024), idesc, k * 16 % GRP != 0);
+                for (int j = 0; j < NG; ++j) odd |= (vsr[j] & 0x7C00) == 0x7C00 || (vbr[j] & 0x7C00) == 0x7C00;
+                // V's constants: rows that are not there are zeros.  Where a tile is masked, a row that is not finite
+                // is zeros too, and rows that see it become NaN through their score
+                uint32_t vsb[NG];
+#pragma unroll
+                for (int j = 0; j < NG; ++j) vsb[j] = !there || (masked && odd) ? 0u : uint32_t(vsr[j]) | uint32_t(vbr[j]) << 16;
+                // ---- K, and the scores' MMAs
+                if (tile) wait(bar_full, tile - 1);
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) {
+                    const uint4 q = kr[i >> 2];
+                    const uint32_t c = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w, y = c >> 8;
+                    put(F::OFF_K, i, make_uint4(c & 0x000F000Fu, c & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u));
                 }
-                umma_f16_ss(tmem + F::COL_B, smem_desc_noswz(sbase + F::OFF_KB, kPos * 16, 128),
-                            smem_desc_noswz(sbase + F::OFF_QB, N * 16, 128), idesc, 0);
-                umma_commit(bar_s);
-            }
-            // ---- V to shared memory, dequantized; rows that are not there are zeros.  Where a tile is masked,
-            // a row that is not finite is zeros too, and rows that see it become NaN through their score
-            bool odd = false;
+                {  // each group's bias three times, in columns 3 j, 3 j + 1, 3 j + 2
+                    uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < NG; ++j) odd |= (vsr[j] & 0x7C00) == 0x7C00 || (vbr[j] & 0x7C00) == 0x7C00;
-            const bool zero = !mine || (masked && odd);
+                    for (int k = 0; k < 3 * NG; ++k) c[k >> 1] |= there ? uint32_t(kbr[k / 3]) << (16 * (k & 1)) : 0u;
+                    sts_v4(sbase + F::OFF_KB + me * 16, make_uint4(c[0], c[1], c[2], c[3]));
+                    if (3 * NG > 8) sts_v4(sbase + F::OFF_KB + kPos * 16 + me * 16, make_uint4(c[4], c[5], c[6], c[7]));
+                }
+                uint32_t* const pos = reinterpret_cast<uint32_t*>(smem + F::OFF_POS) + (tile & 1) * kPos * (NG + 1) + me;
+                pos[NG * kPos] = (there ? 0u : kAbsent) | (odd ? kOdd : 0u);
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) {
-                const uint4 q = vr[i >> 2];
-                const uint32_t c = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w, y = c >> 8;
-                const uint32_t s = vsr[i * 8 / GRP] * 0x10001u, b = vbr[i * 8 / GRP] * 0x10001u;
-                // 1024 + q and 1024 + 16 q, to q, to s q + b
-                uint4 o;
-                o.x = hfma2(hfma2((c & 0x000F000Fu) | kMagic1024x2, kOnes, kMinus1024x2), s, b);
-                o.y = hfma2(hfma2((c & 0x00F000F0u) | kMagic1024x2, 0x2C002C00u, 0xD400D400u), s, b);
-                o.z = hfma2(hfma2((y & 0x000F000Fu) | kMagic1024x2, kOnes, kMinus1024x2), s, b);
-                o.w = hfma2(hfma2((y & 0x00F000F0u) | kMagic1024x2, 0x2C002C00u, 0xD400D400u), s, b);
-                if (zero) o = make_uint4(0, 0, 0, 0);
-                sts_v4(sbase + F::OFF_V + place(tid, i, F::PANEL), o);
-            }
-            // ---- the next tile's rows are on their way from here on
-            const int u_next = seek(cur, u + 1);
-            if (u_next < cur->n) fetch(cur, u_next);
-            // ---- probabilities
-            wait(bar_s, par_s);
-            tc_fence_after();
-            float p[N];
-            while (true) {
-                float top = -INFINITY;
+                for (int j = 0; j < NG; ++j) pos[j * kPos] = __float_as_uint(__half2float(__ushort_as_half(ksr[j])));
+                fence_async_smem();
+                mbar_arrive(bar_full);
+                group_sync(1);
+                if (tid == kPos) {
+                    if (tile) wait(bar_free, tile - 1);
+                    tc_fence_after();
 #pragma unroll
-                for (int r0 = 0; r0 < N; r0 += 16) {
-                    uint32_t sb[16], sg[NG][16];
-                    tmem_ld16(tmem_row + F::COL_B + r0, sb);
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) tmem_ld16(tmem_row + j * N + r0, sg[j]);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 c = *reinterpret_cast<const float2*>(smem + F::OFF_F + (r0 + k) * 8);
-                        float x = __uint_as_float(sb[k]);
-#pragma unroll
-                        for (int j = 0; j < NG; ++j) x = fmaf(ks[j], __uint_as_float(sg[j][k]), x);
-                        p[r0 + k] = fmaf(c.x, x, -c.y);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = (k & 3) * 32;
+                        umma_f16_ss(tmem + (k * 16 / GRP) * N, smem_desc_sw128(sbase + F::OFF_K + (k >> 2) * F::PANEL + o, 1024),
+                                    smem_desc_sw128(sbase + F::OFF_Q + (k >> 2) * F::QPANEL + o, 1024), idesc, k * 16 % GRP != 0);
                     }
+                    umma_f16_ss(tmem + F::COL_B, smem_desc_noswz(sbase + F::OFF_KB, kPos * 16, 128),
+                                smem_desc_noswz(sbase + F::OFF_QB, N * 16, 128), idesc, 0);
+                    umma_commit(bar_full);
                 }
-                if (masked) {
-                    const bool in = mine && t < cur->keys;
-                    const int d = t - cur->start;
-#pragma unroll
-                    for (int r = 0; r < N; ++r) {
-                        bool on;
-                        if (a.tree != nullptr) {
-                            const int64_t bits = *reinterpret_cast<const int64_t*>(smem + F::OFF_BITS + r * 8);
-                            on = d < 0 || (d < 64 && ((bits >> d) & 1));
-                        } else {
-                            const int lim = *reinterpret_cast<const int*>(smem + F::OFF_LIM + r * 4);
-                            on = t <= lim && (a.window <= 0 || lim == INT_MAX || t > lim - a.window);
-                        }
-                        p[r] = on && in ? (odd ? NAN : p[r]) : -INFINITY;
-                    }
-                } else if (!mine) {  // a page outside the pool
-#pragma unroll
-                    for (int r = 0; r < N; ++r) p[r] = -INFINITY;
+                __syncwarp();
+                if (u_next < cur->n) {
+                    fetch_k(cur, u_next);
+                    look(cur, seek(cur, u_next + 1));
                 }
+                // ---- V
+                if (tile) wait(bar_done, tile - 1);
 #pragma unroll
-                for (int r = 0; r < N; ++r) top = fmaxf(top, p[r]);
-                if (!__syncthreads_or(top > kMaxX)) break;
-                // new references: the largest x of each row becomes 0.  Sums again without a reference
-                float* const red = reinterpret_cast<float*>(smem + F::OFF_RED);
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    // x - ref loses x where ref is kNoRef: the score itself is f * sums
-                    p[r] = p[r] == -INFINITY ? -INFINITY : 0.f;
+                for (int i = 0; i < WORDS; ++i) {
+                    const uint4 q = vr[i >> 2];
+                    const uint32_t c = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w, y = c >> 8;
+                    const uint32_t sb = vsb[i * 8 / GRP], s = __byte_perm(sb, 0, 0x1010), b = __byte_perm(sb, 0, 0x3232);
+                    // 1024 + q and 1024 + 16 q, to q, to s q + b
+                    uint4 o;
+                    o.x = hfma2(hfma2((c & 0x000F000Fu) | kMagic1024x2, kOnes, kMinus1024x2), s, b);
+                    o.y = hfma2(hfma2((c & 0x00F000F0u) | kMagic1024x2, 0x2C002C00u, 0xD400D400u), s, b);
+                    o.z = hfma2(hfma2((y & 0x000F000Fu) | kMagic1024x2, kOnes, kMinus1024x2), s, b);
+                    o.w = hfma2(hfma2((y & 0x00F000F0u) | kMagic1024x2, 0x2C002C00u, 0xD400D400u), s, b);
+                    put(F::OFF_V, i, o);
                 }
-#pragma unroll
-                for (int r0 = 0; r0 < N; r0 += 16) {
-                    uint32_t sb[16], sg[NG][16];
-                    tmem_ld16(tmem_row + F::COL_B + r0, sb);
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) tmem_ld16(tmem_row + j * N + r0, sg[j]);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float x = __uint_as_float(sb[k]);
-#pragma unroll
-                        for (int j = 0; j < NG; ++j) x = fmaf(ks[j], __uint_as_float(sg[j][k]), x);
-                        x *= reinterpret_cast<const float2*>(smem + F::OFF_F)[r0 + k].x;
-                        const float m = warp_max(x + p[r0 + k]);
-                        if (lane == 0) red[w * N + r0 + k] = m;
-                    }
-                }
-                __syncthreads();
-                float* const fr = reinterpret_cast<float*>(smem + F::OFF_F);
-                float f[N];
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    const float was = fr[2 * r + 1];
-                    const float m = fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r]));
-                    f[r] = ex2(was - fmaxf(was, m));
-                    l[r] *= f[r];
-                }
-                __syncthreads();
-                if (tid < N) {
-                    const float m = fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid]));
-                    fr[2 * tid + 1] = fmaxf(fr[2 * tid + 1], m);
-                }
-                if (any_tile) {  // its sums are complete: waited for above
-#pragma unroll
-                    for (int r0 = 0; r0 < N; r0 += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(tmem_row + F::COL_O + r0, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[r0 + k]);
-                        tmem_st_32x32b_x16(tmem_row + F::COL_O + r0, o);
-                    }
-                    tc_wait_st();
-                }
-                __syncthreads();
+                fence_async_smem();
+                mbar_arrive(bar_vfull);
+                if (u_next < cur->n) fetch_v();
+                ++tile;
+                u = u_next;
             }
-#pragma unroll
-            for (int r0 = 0; r0 < N; r0 += 8) {
-                uint4 hi, lo;
-                uint32_t* const h = reinterpret_cast<uint32_t*>(&hi);
-                uint32_t* const q = reinterpret_cast<uint32_t*>(&lo);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p0 = ex2(p[r0 + 2 * k]), p1 = ex2(p[r0 + 2 * k + 1]);
-                    l[r0 + 2 * k] += p0, l[r0 + 2 * k + 1] += p1;
-                    h[k] = f32x2_to_f16x2(p0, p1);
-                    q[k] = f32x2_to_f16x2(p0 - half_lo(h[k]), p1 - half_hi(h[k]));
-                }
-                sts_v4(sbase + F::OFF_K + place(tid, r0 / 8, F::PANEL), hi);
-                if (!a.is_bf16) sts_v4(sbase + F::OFF_K + F::PANEL + place(tid, r0 / 8, F::PANEL), lo);
+            // ---- the next run's first rows are on their way while the softmax warps put this one together
+            const int x = pl.pieces ? x_end : cur->x + cur->n;
+            const bool more = x < x_end;
+            if (more) {
+                bad |= plan_run(a, pl, cut, x, x_end, cur->b, cur->before, false, tid == kPos, next);
+                group_sync(1);
+                u = seek(next, 0);
+                look(next, u);
+                fetch_k(next, u);
+                fetch_v();
+                look(next, seek(next, u + 1));
             }
-            fence_async_smem();
-            tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
-                for (int term = 0; term < (a.is_bf16 ? 1 : 2); ++term)
-#pragma unroll
-                    for (int k = 0; k < kPos / 16; ++k)
-                        umma_f16_ss(tmem + F::COL_O, desc_sw128(sbase + F::OFF_V + k * 2048, F::PANEL, 1024),
-                                    desc_sw128(sbase + F::OFF_K + term * F::PANEL + k * 2048, F::PANEL, 1024), idesc_t,
-                                    any_tile || term || k);
-                umma_commit(bar_o);
-            }
-            any_tile = true;
-            u = u_next;
+            __syncthreads();  // the run's sums are written
+            if (cur->n != cur->units) join_item<D, N>(a, pl, cur, tid, kTcThreads, flag);
+            if (!more) break;
+            __syncthreads();  // Q, the rows' constants and red are free
+            Run* const was = cur;
+            cur = next;
+            next = was;
         }
-        if (any_tile) wait(bar_o, par_o);
-        tc_fence_after();
-
-        // ---- the next item's first rows are on their way while this one is put together
-        const int x = pl.pieces ? x_end : cur->x + cur->n;
-        const bool more = x < x_end;
-        if (more) {
-            bad |= plan_run(a, pl, cut, x, x_end, cur->b, cur->before, false, tid == 0, next);
-        }
+    } else {
+        // ================================================= softmax: the scores of a position a thread
+        if constexpr (F::SPLIT) regs_up<kRegsS>();
         float* const red = reinterpret_cast<float*>(smem + F::OFF_RED);
+        float* const nref = reinterpret_cast<float*>(smem + F::OFF_NREF);
+        while (true) {
+            stage_q();
+            __syncthreads();
+            uint64_t l[N / 2];  // pairs of rows
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-            float v = l[r];
+            for (int r = 0; r < N / 2; ++r) l[r] = pair(0.f, 0.f);
+            bool any_tile = false;
+            int u = seek(cur, 0);
+            while (u < cur->n) {
+                const int t = cur->t0 + kPos * u + me;
+                const bool masked = !(cur->t0 + kPos * u >= cur->full_lo && cur->t0 + kPos * (u + 1) <= cur->full_hi);
+                wait(bar_full, tile);
+                tc_fence_after();
+                const uint32_t* const pos = reinterpret_cast<const uint32_t*>(smem + F::OFF_POS) + (tile & 1) * kPos * (NG + 1) + me;
+                const uint32_t state = pos[NG * kPos];
+                uint64_t ks[NG];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-            if (lane == 0) red[w * N + r] = v;
-        }
-        __syncthreads();
-        if (more) {
-            u = seek(next, 0);
-            fetch(next, u);
-        }
-        const bool whole = cur->n == cur->units;
-        float* const slot = a.part + int64_t(attn_slot(blockIdx.x, cur->first)) * F::SLOT;
-        // this thread's d: the codes' order within a word
-        const int pos = tid & 7, d = (tid & ~7) + (pos >> 1) + (pos & 1) * 4;
-        const float* const fr = reinterpret_cast<const float*>(smem + F::OFF_F);
+                for (int j = 0; j < NG; ++j) ks[j] = bits2(pos[j * kPos], pos[j * kPos]);
+                // half of the rows at a time where there are 64
 #pragma unroll
-        for (int r0 = 0; r0 < N; r0 += 16) {
-            if (r0 >= cur->rows) break;
-            uint32_t o[16];
-            tmem_ld16(tmem_row + F::COL_O + r0, o);
-            tc_wait_ld();
+                for (int h0 = 0; h0 < N; h0 += HR) {
+                    uint32_t see = state & kAbsent ? 0u : 0xFFFFFFFFu;  // rows of this half that see the position
+                    if (masked && see) {
+                        const int d = t - cur->start;
+                        see = 0;
+                        if (t < cur->keys) {
+#pragma unroll 1
+                            for (int r = 0; r < HR; ++r) {
+                                bool on;
+                                if (a.tree != nullptr) {
+                                    const int64_t bits = *reinterpret_cast<const int64_t*>(smem + F::OFF_BITS + (h0 + r) * 8);
+                                    on = d < 0 || (d < 64 && ((bits >> d) & 1));
+                                } else {
+                                    const int lim = *reinterpret_cast<const int*>(smem + F::OFF_LIM + (h0 + r) * 4);
+                                    on = t <= lim && (a.window <= 0 || lim == INT_MAX || t > lim - a.window);
+                                }
+                                see |= uint32_t(on) << r;
+                            }
+                        }
+                    }
+                    const bool all = see == 0xFFFFFFFFu && !(masked && (state & kOdd));
+                    // the sums of rows [r0, r0 + CH) of this half, as a ring of two: one is read while the other is used
+                    uint32_t sb[2][CH], sg[2][NG][CH];
+                    auto read = [&](int at, int r0) {
+                        tmem_ld(tmem_row + F::COL_B + h0 + r0, sb[at]);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int r = r0 + k;
-                if (r >= cur->rows || tid >= D) continue;
-                const float ls = (red[r] + red[N + r]) + (red[2 * N + r] + red[3 * N + r]);
-                const float v = any_tile ? __uint_as_float(o[k]) : 0.f;
-                if (whole) {
-                    const int qr = cur->row_lo + r, tok = qr / a.group_heads;
-                    const int head = cur->h * a.group_heads + qr - tok * a.group_heads;
-                    const float out = ls == 0.f ? 0.f : v / ls;
-                    uint16_t* dst = a.o + int64_t(cur->row0 + tok) * a.o_ts + int64_t(head) * a.o_hs + d;
-                    *dst = a.is_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(out)) : __half_as_ushort(__float2half_rn(out));
-                    if (tid == 0 && a.lse != nullptr)
-                        a.lse[int64_t(cur->row0 + tok) * (a.kv_heads * a.group_heads) + head] =
-                            ls == 0.f ? -INFINITY : (fr[2 * r + 1] + lg2(ls)) * 0.693147180559945309f;
-                } else {
-                    __stcg(slot + r * D + d, v);
-                    if (tid == 0) __stcg(slot + N * D + r, fr[2 * r + 1]), __stcg(slot + N * D + N + r, ls);
+                        for (int j = 0; j < NG; ++j) tmem_ld(tmem_row + j * N + h0 + r0, sg[at][j]);
+                    };
+                    float p[HR];
+                    while (true) {
+                        float top = -INFINITY;
+                        read(0, 0);
+#pragma unroll
+                        for (int r0 = 0; r0 < HR; r0 += CH) {
+                            const int at = r0 / CH & 1;
+                            tc_wait_ld();
+                            if (r0 + CH < HR) read(at ^ 1, r0 + CH);
+#pragma unroll
+                            for (int k = 0; k < CH; k += 4) {
+                                const uint4 f4 = lds_v4(sbase + F::OFF_F + (h0 + r0 + k) * 4), n4 = lds_v4(sbase + F::OFF_NREF + (h0 + r0 + k) * 4);
+                                const uint64_t f[2] = {bits2(f4.x, f4.y), bits2(f4.z, f4.w)}, n[2] = {bits2(n4.x, n4.y), bits2(n4.z, n4.w)};
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int i = k + 2 * h;
+                                    uint64_t x = bits2(sb[at][i], sb[at][i + 1]);
+#pragma unroll
+                                    for (int j = 0; j < NG; ++j) x = fma2(ks[j], bits2(sg[at][j][i], sg[at][j][i + 1]), x);
+                                    const float2 y = unpair(fma2(f[h], x, n[h]));
+                                    p[r0 + i] = y.x, p[r0 + i + 1] = y.y;
+                                }
+                            }
+                        }
+                        if (!all) {
+                            const bool odd = masked && (state & kOdd);
+#pragma unroll
+                            for (int r = 0; r < HR; ++r) p[r] = (see >> r) & 1 ? (odd ? NAN : p[r]) : -INFINITY;
+                        }
+#pragma unroll
+                        for (int r = 0; r < HR; ++r) top = fmaxf(top, p[r]);
+                        if (!group_or(2, top > kMaxX)) break;
+                        // new references: the largest x of each row becomes 0.  x - ref has lost x where there was no
+                        // reference yet, so the scores are taken from the sums again
+                        if (any_tile) wait(bar_done, tile - 1);  // O is rescaled
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int r0 = 0; r0 < HR; r0 += CH) {
+                            read(0, r0);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < CH; ++k) {
+                                float x = __uint_as_float(sb[0][k]);
+#pragma unroll
+                                for (int j = 0; j < NG; ++j) x = fmaf(unpair(ks[j]).x, __uint_as_float(sg[0][j][k]), x);
+                                x *= reinterpret_cast<const float*>(smem + F::OFF_F)[h0 + r0 + k];
+                                const float m = warp_max((see >> (r0 + k)) & 1 ? x : -INFINITY);
+                                if (lane == 0) red[w * N + h0 + r0 + k] = m;
+                            }
+                        }
+                        group_sync(2);
+                        if (tid < HR) {  // the factor of what there is, in red's first row
+                            const int r = h0 + tid;
+                            const float was = -nref[r];
+                            const float now = fmaxf(was, fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])));
+                            red[r] = ex2(was - now);
+                            nref[r] = -now;
+                        }
+                        group_sync(2);
+#pragma unroll
+                        for (int r = 0; r < HR; r += 4) {
+                            const uint4 f = lds_v4(sbase + F::OFF_RED + (h0 + r) * 4);
+                            l[(h0 + r) / 2] = mul2(l[(h0 + r) / 2], bits2(f.x, f.y));
+                            l[(h0 + r) / 2 + 1] = mul2(l[(h0 + r) / 2 + 1], bits2(f.z, f.w));
+                        }
+                        if (any_tile) {
+#pragma unroll 1
+                            for (int r0 = 0; r0 < HR; r0 += CH) {
+                                uint32_t o[CH];
+                                tmem_ld(tmem_row + F::COL_O + h0 + r0, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < CH; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[h0 + r0 + k]);
+                                tmem_st(tmem_row + F::COL_O + h0 + r0, o);
+                                tc_wait_st();
+                            }
+                        }
+                        group_sync(2);
+                    }
+                    if (h0 + HR == N) {
+                        tc_fence_before();
+                        mbar_arrive(bar_free);
+                    }
+                    if (any_tile && h0 == 0) wait(bar_done, tile - 1);  // P's place is free
+#pragma unroll
+                    for (int r0 = 0; r0 < HR; r0 += 8) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float p0 = ex2(p[r0 + 2 * k]), p1 = ex2(p[r0 + 2 * k + 1]);
+                            l[(h0 + r0) / 2 + k] = add2(l[(h0 + r0) / 2 + k], pair(p0, p1));
+                            h[k] = f32x2_to_f16x2(p0, p1);
+                            p[r0 + 2 * k] = p0, p[r0 + 2 * k + 1] = p1;
+                        }
+                        sts_v4(own[(h0 + r0) / 8] + F::OFF_P, make_uint4(h[0], h[1], h[2], h[3]));
+                        if (N <= 32 && !a.is_bf16) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) h[k] = f32x2_to_f16x2(p[r0 + 2 * k] - half_lo(h[k]), p[r0 + 2 * k + 1] - half_hi(h[k]));
+                            sts_v4(own[(4 + r0 / 8) & 7] + F::OFF_P, make_uint4(h[0], h[1], h[2], h[3]));
+                        }
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                group_sync(2);
+                if (tid == 0) {
+                    wait(bar_vfull, tile);
+                    tc_fence_after();
+                    for (int term = 0; term < (N > 32 || a.is_bf16 ? 1 : 2); ++term)
+#pragma unroll
+                        for (int k = 0; k < kPos / 16; ++k)
+                            umma_f16_ss(tmem + F::COL_O, desc_sw128(sbase + F::OFF_V + k * 2048, F::PANEL, 1024),
+                                        desc_sw128(sbase + F::OFF_P + term * 64 + k * 2048, F::PANEL, 1024), idesc_t,
+                                        any_tile || term || k);
+                    umma_commit(bar_done);
+                }
+                __syncwarp();
+                any_tile = true;
+                ++tile;
+                u = seek(cur, u + 1);
+            }
+            const bool more = !pl.pieces && cur->x + cur->n < x_end;
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                float v = r & 1 ? unpair(l[r / 2]).y : unpair(l[r / 2]).x;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+                if (lane == 0) red[w * N + r] = v;
+            }
+            group_sync(2);
+            if (any_tile) wait(bar_done, tile - 1);
+            tc_fence_after();
+            const bool whole = cur->n == cur->units;
+            float* const slot = a.part + int64_t(attn_slot(blockIdx.x, cur->first)) * F::SLOT;
+            // this thread's d: the codes' order within a word
+            const int o8 = me & 7, d = (me & ~7) + (o8 >> 1) + (o8 & 1) * 4;
+#pragma unroll 1
+            for (int r0 = 0; r0 < N; r0 += CH) {
+                if (r0 >= cur->rows) break;
+                uint32_t o[CH];
+                tmem_ld(tmem_row + F::COL_O + r0, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int r = r0 + k;
+                    if (r >= cur->rows || me >= D) continue;
+                    const float ls = (red[r] + red[N + r]) + (red[2 * N + r] + red[3 * N + r]);
+                    const float v = any_tile ? __uint_as_float(o[k]) : 0.f;
+                    if (whole) {
+                        const int qr = cur->row_lo + r, tok = qr / a.group_heads;
+                        const int head = cur->h * a.group_heads + qr - tok * a.group_heads;
+                        const float out = ls == 0.f ? 0.f : v / ls;
+                        uint16_t* dst = a.o + int64_t(cur->row0 + tok) * a.o_ts + int64_t(head) * a.o_hs + d;
+                        *dst = a.is_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(out)) : __half_as_ushort(__float2half_rn(out));
+                        if (me == 0 && a.lse != nullptr)
+                            a.lse[int64_t(cur->row0 + tok) * (a.kv_heads * a.group_heads) + head] =
+                                ls == 0.f ? -INFINITY : (lg2(ls) - nref[r]) * 0.693147180559945309f;
+                    } else {
+                        __stcg(slot + r * D + d, v);
+                        if (me == 0) __stcg(slot + N * D + r, -nref[r]), __stcg(slot + N * D + N + r, ls);
+                    }
                 }
             }
+            tc_fence_before();
+            if (!whole) __threadfence();
+            __syncthreads();  // the run's sums are written
+            if (!whole) join_item<D, N>(a, pl, cur, tid, kTcThreads, flag);
+            if (!more) break;
+            __syncthreads();  // Q, the rows' constants and red are free
+            Run* const was = cur;
+            cur = next;
+            next = was;
         }
-        tc_fence_before();
-        if (!whole) join_item<D, N>(a, pl, cur, tid, kPos, flag);
-        if (!more) break;
-        __syncthreads();  // Q, the rows' constants and red are free
-        Run* const was = cur;
-        cur = next;
-        next = was;
     }
     __syncthreads();
     if (w == 0) tmem_dealloc(tmem, F::COLS);
@@ -524,8 +677,9 @@ bool attn_tc_supported(int head_dim) { return head_dim == 64 || head_dim == 128;
 
 cudaError_t launch_attn_tc(const AttnArgs& in, int head_dim, int group, int64_t rows, cudaStream_t stream) {
     AttnArgs a = in;
-    const TcAttnInst k = instance(head_dim, group, rows <= 16 ? 16 : rows <= 32 ? 32 : 64);
-    return launch_attn_blocks(a, k.fn, kPos, k.smem, k.slot, k.rows, kAttnTcUnit, stream);
+    // 64 rows at a time only with P in one term
+    const TcAttnInst k = instance(head_dim, group, rows <= 16 ? 16 : rows <= 32 || !a.is_bf16 ? 32 : 64);
+    return launch_attn_blocks(a, k.fn, kTcThreads, k.smem, k.slot, k.rows, kAttnTcUnit, k.rows > 32 ? 128 : 0, stream);
 }
 
 cudaError_t attn_tc_read_and_clear_errors(unsigned* out) {
