@@ -601,11 +601,9 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
         __syncwarp();
 
         // ---- the next item's first tiles are fetched while this one's sums are put together
-        const int x = pl.pieces ? x_end : cur->x + cur->n;
-        const bool more = x < x_end;
+        const bool more = plan_run(a, pl, cut, cur->x + cur->places, x_end, cur->b, cur->before, lane == 0, next, &bad);
+        __syncwarp();
         if (more) {
-            bad |= plan_run(a, pl, cut, x, x_end, cur->b, cur->before, false, lane == 0, next);
-            __syncwarp();
             q_first = load_q(next, tid);
             begin(next);
 #pragma unroll
@@ -640,7 +638,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
         __syncthreads();
         // ---- the block's sums: to the output, or to this block's slot of the workspace
         const bool whole = cur->n == cur->units;
-        float* slot_o = a.part + int64_t(attn_slot(blockIdx.x, cur->first)) * F::SLOT;
+        float* slot_o = a.part + int64_t(attn_slot(blockIdx.x, cur->c0)) * F::SLOT;
         for (int i = tid; i < cur->rows * (D / 4); i += THREADS) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
             float rf[W], top = kNoRef;
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
                 if (d == 0) __stcg(slot_o + R * D + row, top), __stcg(slot_o + R * D + R + row, lsum);
             }
         }
-        if (!whole) join_item<D, R>(a, pl, cur, tid, THREADS, reinterpret_cast<int*>(smem + F::OFF_LAST));
+        if (!whole) join_item<D, R>(a, cur, tid, THREADS, reinterpret_cast<int*>(smem + F::OFF_LAST));
         if (!more) break;
         __syncthreads();  // the sums' ring slots and Q are free
         Run* const was = cur;

@@ -101,25 +101,37 @@ struct Run {
     int lo, hi;        // positions that some row sees
     int full_lo, full_hi;  // positions [full_lo, full_hi) that every row sees
     int t0;            // position of the first unit
-    int first;         // the item is the block's first
+    int places;        // from x to the end of this share
     int c0, c1;        // the blocks that share the item
     int x, before;     // place in the order of the blocks; weight of the sequences in front of b
 };
 static_assert(sizeof(Run) <= 96, "Run does not fit its place");
 
 
-// Writes (if `writer`) the share of the item at place x of the order of the blocks, in or after
-// sequence b.  True if the table cannot name all of the sequence's positions.
+// The next run with units at or behind place x of the order of the blocks, in or after sequence b: written
+// by `writer` to *r.  False if the block's share has none (then r->n is 0); *bad if the table cannot name
+// all of the sequence's positions.
 __device__ __forceinline__ bool plan_run(const AttnArgs& a, const AttnPlan& pl, AttnCut cut, int x, int x_end, int b,
-                                         int before, bool first_item, bool writer, Run* r) {
-    AttnSeq s = load_seq(a, b, cut);
-    int weight = attn_seq_weight(pl, s, a.kv_heads);
-    while (x >= before + weight) {
-        before += weight;
-        s = load_seq(a, ++b, cut);
-        weight = attn_seq_weight(pl, s, a.kv_heads);
+                                         int before, bool writer, Run* r, bool* bad) {
+    AttnSeq s;
+    AttnShare sh;
+    sh.n = 0;
+    if (x < x_end) s = load_seq(a, b, cut);
+    while (x < x_end) {
+        const int weight = attn_seq_weight(pl, s, a.kv_heads);
+        if (x >= before + weight) {
+            before += weight;
+            s = load_seq(a, ++b, cut);
+            continue;
+        }
+        sh = attn_share(pl, s, x, x_end, before);
+        if (sh.n > 0) break;
+        x += sh.places;  // only the start of an item: its units are the next block's
     }
-    const AttnShare sh = attn_share(pl, s, x, x_end, before);
+    if (sh.n == 0) {
+        if (writer) r->n = 0;
+        return false;
+    }
     const int h = sh.item / s.rt, row_lo = (sh.item - h * s.rt) * cut.rows, nrows = s.n * a.group_heads;
     const int rows = nrows - row_lo < cut.rows ? nrows - row_lo : cut.rows;
     const int first = s.start + row_lo / a.group_heads, last = s.start + (row_lo + rows - 1) / a.group_heads;
@@ -133,32 +145,30 @@ __device__ __forceinline__ bool plan_run(const AttnArgs& a, const AttnPlan& pl, 
         r->full_hi = all < s.keys ? all : s.keys;
         r->full_lo = a.window > 0 && last >= a.window ? last - a.window + 1 : 0;
         r->t0 = s.lo + cut.unit * sh.u0;
-        r->first = first_item;
-        r->c0 = sh.c0, r->c1 = sh.c1, r->x = x, r->before = before;
+        r->c0 = sh.c0, r->c1 = sh.c1, r->x = x, r->places = sh.places, r->before = before;
     }
-    return s.start + s.n > a.capacity;
+    *bad |= s.start + s.n > a.capacity;
+    return true;
 }
 
 // The block's place in the work: its first run and the end of its share.  0: it has none; 1: go on;
 // -1: the offsets fall, and nothing is done.
 __device__ __forceinline__ int plan_block(const AttnArgs& a, AttnCut cut, int lane, bool writer, AttnPlan* pl, int* x_end,
                                           Run* r, bool* bad) {
-    int total, items, before = 0;
-    if (!all_work(a, cut, lane, &total, &items)) return -1;
-    *pl = attn_plan(total, items, gridDim.x, cut.unit, cut.warps);
+    int units, items, before = 0;
+    if (!all_work(a, cut, lane, &units, &items)) return -1;
+    *pl = attn_plan(units, items, gridDim.x, cut.unit, cut.warps);
     const int x = pl->pieces ? int(blockIdx.x) : int(blockIdx.x) * pl->per;
-    *x_end = pl->pieces ? x + 1 : x + pl->per < total ? x + pl->per : total;
+    *x_end = pl->pieces ? x + 1 : x + pl->per < pl->total ? x + pl->per : pl->total;
     const int b = find_seq(a, *pl, cut, x, lane, &before);
-    if (b >= a.seqs) return 0;
-    *bad = plan_run(a, *pl, cut, x, *x_end, b, before, true, writer, r);
-    return 1;
+    return b < a.seqs && plan_run(a, *pl, cut, x, *x_end, b, before, writer, r, bad) ? 1 : 0;
 }
 
 // Counts this block's sums of an item in (all of the block's threads call it, with its sums written);
 // the last of the item's blocks to arrive adds them in block order and writes the rows.  A slot is
 // [ROWS][D] sums, the rows' references and their l.
 template <int D, int ROWS>
-__device__ __forceinline__ void join_item(const AttnArgs& a, const AttnPlan& pl, const Run* cur, int tid, int threads, int* flag) {
+__device__ __forceinline__ void join_item(const AttnArgs& a, const Run* cur, int tid, int threads, int* flag) {
     const int c0 = cur->c0, c1 = cur->c1;
     __threadfence();
     __syncthreads();
@@ -166,9 +176,7 @@ __device__ __forceinline__ void join_item(const AttnArgs& a, const AttnPlan& pl,
     __syncthreads();
     if (!*flag) return;
     __threadfence();
-    // the item is the first of its blocks, but for c0 where that began in front of it
-    const bool c0_first = pl.pieces || c0 * pl.per == cur->x - cur->u0;
-    auto slot_of = [&](int i) { return a.part + int64_t(attn_slot(i, i > c0 || c0_first)) * (ROWS * (D + 2)); };
+    auto slot_of = [&](int i) { return a.part + int64_t(attn_slot(i, c0)) * (ROWS * (D + 2)); };
     for (int i = tid; i < cur->rows * (D / 4); i += threads) {
         const int row = i / (D / 4), d = i % (D / 4) * 4;
         float top = kNoRef, lsum = 0.f;

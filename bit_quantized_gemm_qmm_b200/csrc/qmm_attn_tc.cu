@@ -399,11 +399,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 u = u_next;
             }
             // ---- the next run's first rows are on their way while the softmax warps put this one together
-            const int x = pl.pieces ? x_end : cur->x + cur->n;
-            const bool more = x < x_end;
+            const bool more = plan_run(a, pl, cut, cur->x + cur->places, x_end, cur->b, cur->before, tid == kPos, next, &bad);
+            group_sync(1);
             if (more) {
-                bad |= plan_run(a, pl, cut, x, x_end, cur->b, cur->before, false, tid == kPos, next);
-                group_sync(1);
                 u = seek(next, 0);
                 look(next, u);
                 fetch_k(next, u);
@@ -411,7 +409,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 look(next, seek(next, u + 1));
             }
             __syncthreads();  // the run's sums are written
-            if (cur->n != cur->units) join_item<D, N>(a, pl, cur, tid, kTcThreads, flag);
+            if (cur->n != cur->units) join_item<D, N>(a, cur, tid, kTcThreads, flag);
             if (!more) break;
             __syncthreads();  // Q, the rows' constants and red are free
             Run* const was = cur;
@@ -592,7 +590,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 ++tile;
                 u = seek(cur, u + 1);
             }
-            const bool more = !pl.pieces && cur->x + cur->n < x_end;
 #pragma unroll
             for (int r = 0; r < N; ++r) {
                 float v = r & 1 ? unpair(l[r / 2]).y : unpair(l[r / 2]).x;
@@ -604,7 +601,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
             if (any_tile) wait(bar_done, tile - 1);
             tc_fence_after();
             const bool whole = cur->n == cur->units;
-            float* const slot = a.part + int64_t(attn_slot(blockIdx.x, cur->first)) * F::SLOT;
+            float* const slot = a.part + int64_t(attn_slot(blockIdx.x, cur->c0)) * F::SLOT;
             // this thread's d: the codes' order within a word
             const int o8 = me & 7, d = (me & ~7) + (o8 >> 1) + (o8 & 1) * 4;
 #pragma unroll 1
@@ -637,8 +634,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
             tc_fence_before();
             if (!whole) __threadfence();
             __syncthreads();  // the run's sums are written
-            if (!whole) join_item<D, N>(a, pl, cur, tid, kTcThreads, flag);
-            if (!more) break;
+            if (!whole) join_item<D, N>(a, cur, tid, kTcThreads, flag);
+            if (next->n == 0) break;  // planned by the other warpgroup
             __syncthreads();  // Q, the rows' constants and red are free
             Run* const was = cur;
             cur = next;

@@ -76,49 +76,64 @@ struct Quantized {
 template <int GRP>
 __device__ __forceinline__ Quantized quantize_word(uint4 u, int is_bf16) {
     const int lane = threadIdx.x & 31;
-    float v[8];
     const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
+    float v[8];
+    uint32_t odd = 0;  // an exponent of ones carries into its sign's place
+    const uint32_t exps = is_bf16 ? 0x7F807F80u : 0x7C007C00u, one = is_bf16 ? 0x00800080u : 0x04000400u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         v[2 * j] = is_bf16 ? bf16lo_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j])));
         v[2 * j + 1] = is_bf16 ? bf16hi_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j] >> 16)));
+        odd |= (raw[j] & exps) + one;
     }
     float lo = v[0], hi = v[0];
-    bool odd = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (v[j] < lo) lo = v[j];
-        if (v[j] > hi) hi = v[j];
-        odd |= !(fabsf(v[j]) < INFINITY);
-    }
+    for (int j = 1; j < 8; ++j) lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
 #pragma unroll
     for (int o = 1; o < GRP / 8; o <<= 1) {
-        const float lo2 = __shfl_xor_sync(kFull, lo, o), hi2 = __shfl_xor_sync(kFull, hi, o);
-        const bool later = lane & o;  // the lanes before this one keep their value on a tie
-        if (later ? !(lo < lo2) : lo2 < lo) lo = lo2;
-        if (later ? !(hi > hi2) : hi2 > hi) hi = hi2;
+        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
     }
-    const unsigned group_lanes = ((1u << (GRP / 8)) - 1u) << (lane & ~(GRP / 8 - 1));
-    odd = (__ballot_sync(kFull, odd) & group_lanes) != 0;
+    const int first_lane = lane & ~(GRP / 8 - 1);
+    const unsigned group_lanes = ((1u << (GRP / 8)) - 1u) << first_lane;
+    bool bad = (__ballot_sync(kFull, (odd & 0x80008000u) != 0) & group_lanes) != 0;
+    if (__any_sync(kFull, lo == 0.f)) {
+        // a zero's sign: the first of the group's zeros in order
+        float z = 1.f;
+#pragma unroll
+        for (int j = 7; j >= 0; --j) z = v[j] == 0.f ? v[j] : z;
+        const unsigned with = __ballot_sync(kFull, z == 0.f) & group_lanes;
+        z = __shfl_sync(kFull, z, with ? __ffs(with) - 1 : lane);
+        if (lo == 0.f) lo = z;
+    }
     Quantized r;
     r.s = __half_as_ushort(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
     r.b = __half_as_ushort(__float2half_rn(lo));
-    odd |= (r.s & 0x7C00) == 0x7C00 || (r.b & 0x7C00) == 0x7C00;
-    if (odd) r.s = r.b = 0x7FFF;
+    bad |= (r.s & 0x7C00) == 0x7C00 || (r.b & 0x7C00) == 0x7C00;
+    if (bad) r.s = r.b = 0x7FFF;
     const float s = __half2float(__ushort_as_half(r.s)), bf = __half2float(__ushort_as_half(r.b));
     r.word = 0;
-    if (!odd && s != 0.f) {
-        // rint(RN(d / s)) from d * RN(1 / s), which is within 2^-22 of d / s in relative terms (two
-        // roundings): it has the same nearest whole number unless it lies within 2^-12 of a half (codes
-        // are clamped at 15, so only quotients below 16 matter); there the division itself decides
+    if (!bad && s != 0.f) {
+        // rint(RN(d / s)) from t = d * RN(1 / s), which is within 2^-22 of d / s in relative terms (two
+        // roundings): clamped to [0, 15] it has the same nearest whole number unless it lies within 2^-12 of
+        // a half; where one of the eight does, the divisions themselves decide
         const float inv = __frcp_rn(s);
+        constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+        float off = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float d = __fsub_rn(v[j], bf);
-            float t = d * inv;
-            const float f = t - floorf(t);
-            if (fabsf(f - 0.5f) < 0.000244140625f) t = __fdiv_rn(d, s);
-            r.word |= uint32_t(clamp_int(__float2int_rn(t), 0, 15)) << (4 * j);
+            const float t = fminf(fmaxf(__fsub_rn(v[j], bf) * inv, 0.f), 15.f), w = __fadd_rn(t, kWhole);
+            off = fmaxf(off, fabsf(t - __fsub_rn(w, kWhole)));
+            r.word |= (__float_as_uint(w) & 15u) << (4 * j);
+        }
+        if (off > 0.5f - 0.000244140625f) {
+            r.word = 0;
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t h = (raw[j >> 1] >> (16 * (j & 1))) & 0xFFFF;
+                const float x = is_bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(uint16_t(h)));
+                r.word |= uint32_t(clamp_int(__float2int_rn(__fdiv_rn(__fsub_rn(x, bf), s)), 0, 15)) << (4 * j);
+            }
         }
     }
     return r;

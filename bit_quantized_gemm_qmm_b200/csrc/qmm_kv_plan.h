@@ -63,39 +63,41 @@ QMM_HD int attn_seq_units(const AttnSeq& s, int kv_heads) { return attn_seq_item
 
 QMM_HD int ceil_div_int(int a, int b) { return (a - 1) / b + 1; }  // a >= 1
 
-// How the work is dealt out over `blocks` blocks.  Even shares: block i takes units [i * per,
-// (i + 1) * per) of all, across items; a block whose share holds the end of one item and the start of
-// the next changes items, which costs about as much as kAttnChange positions.  Pieces, where items are
-// few: each item is cut into pieces of `per` units (the last one shorter), one a block, so that no
-// block changes items; the pieces are as small as keeps their number within the blocks, and give each
-// of a block's warps a unit at least.
+// How the work is dealt out over `blocks` blocks.  To begin an item costs a block about as much as
+// kAttnChange positions (its query rows, its sums and their join), so an item weighs its units and that.
+// Even shares: block i takes places [i * per, (i + 1) * per) of all items' weights, laid end to end, each
+// item's start before its units.  Pieces, where items are few: each item is cut into pieces of `per` units
+// (the last one shorter), one a block, so that no block changes items; the pieces are as small as keeps
+// their number within the blocks, and give each of a block's warps a unit at least.
 constexpr int kAttnChange = 384;
 struct AttnPlan {
-    int total, per, pieces;  // units of all; units a block; 1: pieces
+    int total, per, pieces, start;  // weight of all; weight a block (units, in pieces); 1: pieces; an item's start
 };
-QMM_HD AttnPlan attn_plan(int total, int items, int blocks, int unit, int warps) {
+QMM_HD AttnPlan attn_plan(int units, int items, int blocks, int unit, int warps) {
     AttnPlan p;
-    p.total = total;
+    p.start = kAttnChange / unit;
+    p.total = units + items * p.start;
     p.pieces = 0;
-    p.per = total < 1 ? 1 : ceil_div_int(total, blocks);
-    if (total > 0 && items < blocks) {
-        int piece = ceil_div_int(total, blocks - items);
+    p.per = p.total < 1 ? 1 : ceil_div_int(p.total, blocks);
+    if (units > 0 && items < blocks) {
+        int piece = ceil_div_int(units, blocks - items);
         if (piece < warps) piece = warps;
-        if (piece <= p.per + kAttnChange / unit) p.pieces = 1, p.per = piece;
+        if (piece <= p.per) p.pieces = 1, p.per = piece;
     }
     return p;
 }
 
 // Weight of a sequence in the order of the blocks: what find_seq adds up.
 QMM_HD int attn_seq_weight(const AttnPlan& p, const AttnSeq& s, int kv_heads) {
-    return p.pieces ? attn_seq_items(s, kv_heads) * ceil_div_int(s.units, p.per) : attn_seq_units(s, kv_heads);
+    return attn_seq_items(s, kv_heads) * (p.pieces ? ceil_div_int(s.units, p.per) : s.units + p.start);
 }
 
-// A block's share of an item.  x: the place in the order of the blocks (the block itself, or a unit),
-// `before` the weight of the sequences in front.
+// A block's share of an item.  x: the place in the order of the blocks (the block itself, or a place in the
+// weights), `before` the weight of the sequences in front.
 struct AttnShare {
-    int item, u0, n;  // item of the sequence, first unit, units
-    int c0, c1;       // the blocks that share the item
+    int item, u0, n;  // item of the sequence, first unit, units (0: of its start alone)
+    int c0, c1;       // the blocks that have units of the item
+    int places;       // from x to the end of the share
 };
 QMM_HD AttnShare attn_share(const AttnPlan& p, const AttnSeq& s, int x, int x_end, int before) {
     AttnShare h;
@@ -107,12 +109,17 @@ QMM_HD AttnShare attn_share(const AttnPlan& p, const AttnSeq& s, int x, int x_en
         h.n = s.units - h.u0 < p.per ? s.units - h.u0 : p.per;
         h.c0 = before + h.item * np;
         h.c1 = h.c0 + np - 1;
+        h.places = 1;
     } else {
-        h.item = in / s.units;
-        h.u0 = in - h.item * s.units;
-        h.n = s.units - h.u0 < x_end - x ? s.units - h.u0 : x_end - x;
-        h.c0 = (x - h.u0) / p.per;
-        h.c1 = (x - h.u0 + s.units - 1) / p.per;
+        const int w = s.units + p.start;
+        h.item = in / w;
+        const int at = in - h.item * w, end = w - at < x_end - x ? w : at + (x_end - x);
+        h.u0 = at > p.start ? at - p.start : 0;
+        h.n = end > p.start ? end - p.start - h.u0 : 0;
+        const int first = x - at + p.start;  // place of the item's first unit
+        h.c0 = first / p.per;
+        h.c1 = (first + s.units - 1) / p.per;
+        h.places = end - at;
     }
     return h;
 }
@@ -134,9 +141,8 @@ QMM_HD void attn_warp_units(int t0, int n, int w, int warps, int lo, int hi, int
     *j1 = last < mine ? last : mine;
 }
 
-// A block writes the sums of an item it does not take whole to one of two slots: those of the first
-// item of its share to slot 2 i, of its last to 2 i + 1 (those between are whole).  An item is the
-// first of each of its blocks but perhaps c0.
-QMM_HD int attn_slot(int block, bool first_item) { return 2 * block + (first_item ? 0 : 1); }
+// A block writes the sums of an item it does not take whole to one of two slots: 2 i + 1 if the item's
+// first unit is its own, else 2 i (there are no others: items between are whole).
+QMM_HD int attn_slot(int block, int c0) { return 2 * block + (block == c0 ? 1 : 0); }
 
 }  // namespace qmm_impl

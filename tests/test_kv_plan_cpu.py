@@ -22,48 +22,49 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
                     int window, int tree, int blocks, int unit, int warps) {
     std::vector<AttnSeq> s;
     std::vector<int> item0, unit0;  // items and units in front of each sequence
-    int total = 0, items = 0;
+    int units = 0, items = 0;
     for (int b = 0; b < seqs; ++b) {
         if (cu[b + 1] < cu[b]) return 0;  // nothing is done
         s.push_back(attn_seq(cu[b], cu[b + 1], lens[b], tokens, capacity, gh, rows, unit, window));
         const AttnSeq& q = s.back();
         if (q.row0 < 0 || q.n < 0 || q.row0 + q.n > tokens || q.keys < 0 || q.keys > capacity) return 1;
         if (q.lo < 0 || q.lo % kAttnSub || q.lo > q.keys || q.units < 1) return 2;
-        item0.push_back(items), unit0.push_back(total);
-        total += attn_seq_units(q, kv_heads);
+        item0.push_back(items), unit0.push_back(units);
+        units += attn_seq_units(q, kv_heads);
         items += attn_seq_items(q, kv_heads);
     }
-    const AttnPlan p = attn_plan(total, items, blocks, unit, warps);
+    const AttnPlan p = attn_plan(units, items, blocks, unit, warps);
     if (p.per < 1) return 3;
-    std::vector<int> taken(total, 0), slots(2 * blocks, -1);  // slot -> item
-    struct Shared { int c0, c1, first; };
-    std::vector<Shared> shared(items, Shared{-1, -1, 0});
+    std::vector<int> taken(units, 0), slots(2 * blocks, -1);  // slot -> item
+    struct Shared { int c0, c1; };
+    std::vector<Shared> shared(items, Shared{-1, -1});
     int order = 0;
     for (int b = 0; b < seqs; ++b) order += attn_seq_weight(p, s[b], kv_heads);
     if (p.pieces && order > blocks) return 4;
-    if (!p.pieces && (int64_t)blocks * p.per < total) return 5;
+    if (!p.pieces && (order != p.total || (int64_t)blocks * p.per < order)) return 5;
     for (int i = 0; i < blocks; ++i) {
         int x = p.pieces ? i : i * p.per;
-        const int end = p.pieces ? x + 1 : x + p.per < total ? x + p.per : total;
+        const int end = p.pieces ? x + 1 : x + p.per < order ? x + p.per : order;
         if (x >= order) continue;
         int b = 0, before = 0;
-        bool first = true;
         while (x < end) {
             const int weight = attn_seq_weight(p, s[b], kv_heads);
             if (x >= before + weight) { before += weight; if (++b >= seqs) return 6; continue; }
             const AttnShare h = attn_share(p, s[b], x, end, before);
-            if (h.item < 0 || h.item >= s[b].rt * kv_heads || h.u0 < 0 || h.n < 1 || h.u0 + h.n > s[b].units) return 7;
+            if (h.places < 1) return 23;
+            if (h.item < 0 || h.item >= s[b].rt * kv_heads || h.u0 < 0 || h.n < 0 || h.u0 + h.n > s[b].units) return 7;
+            if (h.n == 0) { x += h.places; continue; }
             if (i < h.c0 || i > h.c1 || h.c1 >= blocks) return 8;
             if ((h.n == s[b].units) != (h.c0 == h.c1)) return 9;
+            if ((h.u0 == 0) != (i == h.c0)) return 24;
             for (int u = 0; u < h.n; ++u) ++taken[unit0[b] + h.item * s[b].units + h.u0 + u];
             const int id = item0[b] + h.item;
             if (h.n != s[b].units) {
-                const int slot = attn_slot(i, first);
+                const int slot = attn_slot(i, h.c0);
                 if (slot < 0 || slot >= 2 * blocks || slots[slot] != -1) return 10;
                 slots[slot] = id;
-                const int c0_first = p.pieces || h.c0 * p.per == x - h.u0;
-                if (shared[id].c0 >= 0 && (shared[id].c0 != h.c0 || shared[id].c1 != h.c1 || shared[id].first != c0_first)) return 11;
-                shared[id] = Shared{h.c0, h.c1, c0_first};
+                if (shared[id].c0 >= 0 && (shared[id].c0 != h.c0 || shared[id].c1 != h.c1)) return 11;
+                shared[id] = Shared{h.c0, h.c1};
             }
             // tiles of the run
             const int rt = h.item % s[b].rt, r0 = rt * rows, nr = s[b].n * gh - r0 < rows ? s[b].n * gh - r0 : rows;
@@ -89,11 +90,10 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
                 if (unit == kAttnUnit && by[u] != (any ? 1 : 0)) return 17;
                 if (t < 0 || t % kAttnSub) return 18;
             }
-            x = p.pieces ? end : x + h.n;
-            first = false;
+            x += h.places;
         }
     }
-    for (int u = 0; u < total; ++u) if (taken[u] != 1) return 19;
+    for (int u = 0; u < units; ++u) if (taken[u] != 1) return 19;
     // the join: an item's blocks c0..c1 read the slots that they wrote, and no two items share a counter
     std::vector<int> counter(blocks, -1), read(2 * blocks, 0);
     for (int id = 0; id < items; ++id) {
@@ -101,7 +101,7 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
         if (counter[shared[id].c0] != -1) return 20;
         counter[shared[id].c0] = id;
         for (int i = shared[id].c0; i <= shared[id].c1; ++i) {
-            const int slot = attn_slot(i, i > shared[id].c0 || shared[id].first);
+            const int slot = attn_slot(i, shared[id].c0);
             if (slots[slot] != id) return 21;
             read[slot] = 1;
         }
