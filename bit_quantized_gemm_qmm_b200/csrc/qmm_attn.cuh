@@ -44,9 +44,10 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int row, int head,
             l == 0.f ? -INFINITY : (ref + lg2(l)) * 0.693147180559945309f;
 }
 
-// How a kernel cuts the work: query rows a tile, positions a unit, warps that take units of their own.
+// How a kernel cuts the work: query rows a tile, positions a unit, warps that take units of their own, and what
+// an item's start costs in units.
 struct AttnCut {
-    int rows, unit, warps;
+    int rows, unit, warps, start;
 };
 
 __device__ __forceinline__ AttnSeq load_seq(const AttnArgs& a, int b, AttnCut cut) {
@@ -157,7 +158,7 @@ __device__ __forceinline__ int plan_block(const AttnArgs& a, AttnCut cut, int la
                                           Run* r, bool* bad) {
     int units, items, before = 0;
     if (!all_work(a, cut, lane, &units, &items)) return -1;
-    *pl = attn_plan(units, items, gridDim.x, cut.unit, cut.warps);
+    *pl = attn_plan(units, items, gridDim.x, cut.start, cut.warps);
     const int x = pl->pieces ? int(blockIdx.x) : int(blockIdx.x) * pl->per;
     *x_end = pl->pieces ? x + 1 : x + pl->per < pl->total ? x + pl->per : pl->total;
     const int b = find_seq(a, *pl, cut, x, lane, &before);

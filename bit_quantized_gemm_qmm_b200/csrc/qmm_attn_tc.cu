@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
 
     grid_dependency_wait();
 
-    constexpr AttnCut cut{N, kPos, 1};
+    constexpr AttnCut cut{N, kPos, 1, 2};
     AttnPlan pl;
     int x_end;
     Run* cur = reinterpret_cast<Run*>(smem + F::OFF_RUN);

@@ -46,62 +46,95 @@ __device__ __forceinline__ int64_t cache_row(const KvArgs& a, int b, int pos, in
     return (int64_t(page) * a.kv_heads + h) * a.page + (pos - col * a.page);
 }
 
-// A thread's word (eight values) of the token axis: token, head and place in the row.  Row counts stay
-// below 2^28 (2^20 tokens, 256 heads), so only the word number needs 64 bits.
-struct Word {
-    int tok, h, p8;
+// A thread's NW words (eight values each) of the token axis: token, head and place in the row.  Row counts
+// stay below 2^28 (2^20 tokens, 256 heads), so only the number of the words needs 64 bits.
+struct Words {
+    int tok, h, at;  // at: first of the values
     bool on;
 };
-__device__ __forceinline__ Word my_word(const KvArgs& a) {
-    const int lg = a.dim == 64 ? 3 : a.dim == 128 ? 4 : 5;
+template <int NW>
+__device__ __forceinline__ Words my_words(const KvArgs& a) {
+    const int lg = (a.dim == 64 ? 3 : a.dim == 128 ? 4 : 5) - (NW - 1);
     const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
     const int row = int(i >> lg);
-    Word w;
+    Words w;
     w.on = row < a.tokens * a.kv_heads;
-    w.p8 = int(i) & ((1 << lg) - 1);
+    w.at = (int(i) & ((1 << lg) - 1)) * (8 * NW);
     w.tok = w.on ? row / a.kv_heads : a.tokens - 1;
     w.h = w.on ? row - w.tok * a.kv_heads : 0;
     return w;
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // ---------------------------------------------------------------- append
-// One thread the same eight values of K and of V; a group's range is found by its GRP / 8 lanes.  Each
-// step is the scheme of qmm_quant.cu, rounded the same way, so the bits are those of qmm_quantize (its
+// One thread the same one or two words of K and of V; a group's range is found by the lanes that share it.
+// Two words halve what a thread spends on finding its rows; one is faster while the threads do not fill the
+// GPU (64 tokens of 8 heads of 128: 3.6 us against 5.5; 8,191 tokens: 29 against 23).  The steps are the scheme of qmm_quant.cu, rounded the same way, so the bits are those of qmm_quantize (its
 // scan keeps the first of equal extremes, which decides the sign of a zero: so does this one).  A group
 // with an infinity or NaN, or whose scale or bias leaves fp16, is stored so that it reads as NaN.
 struct Quantized {
-    uint32_t word;
+    uint32_t w[2];
     uint16_t s, b;
 };
-template <int GRP>
-__device__ __forceinline__ Quantized quantize_word(uint4 u, int is_bf16) {
+template <bool BF>
+__device__ __forceinline__ float value_of(uint32_t h) {
+    return BF ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(uint16_t(h)));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (BF) asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <int GRP, bool BF, int NW>
+__device__ __forceinline__ Quantized quantize_words(const uint32_t (&raw)[4 * NW]) {
+    constexpr int LANES = GRP / (8 * NW);  // that share a group
     const int lane = threadIdx.x & 31;
-    const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
-    float v[8];
-    uint32_t odd = 0;  // an exponent of ones carries into its sign's place
-    const uint32_t exps = is_bf16 ? 0x7F807F80u : 0x7C007C00u, one = is_bf16 ? 0x00800080u : 0x04000400u;
+    // the range in 16 bits (its ends are values): least of v in the low half, least of -v in the high half
+    constexpr uint32_t exps = BF ? 0x7F807F80u : 0x7C007C00u, one = BF ? 0x00800080u : 0x04000400u;
+    uint32_t odd = 0, up = raw[0], down = raw[0] ^ 0x80008000u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = is_bf16 ? bf16lo_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j])));
-        v[2 * j + 1] = is_bf16 ? bf16hi_to_f32(raw[j]) : __half2float(__ushort_as_half(uint16_t(raw[j] >> 16)));
-        odd |= (raw[j] & exps) + one;
+    for (int j = 0; j < 4 * NW; ++j) {
+        odd |= (raw[j] & exps) + one;  // an exponent of ones carries into its sign's place
+        up = min2<BF>(up, raw[j]), down = min2<BF>(down, raw[j] ^ 0x80008000u);
     }
-    float lo = v[0], hi = v[0];
+    uint32_t ends = min2<BF>(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
 #pragma unroll
-    for (int j = 1; j < 8; ++j) lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
-#pragma unroll
-    for (int o = 1; o < GRP / 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-    }
-    const int first_lane = lane & ~(GRP / 8 - 1);
-    const unsigned group_lanes = ((1u << (GRP / 8)) - 1u) << first_lane;
+    for (int o = 1; o < LANES; o <<= 1) ends = min2<BF>(ends, __shfl_xor_sync(kFull, ends, o));
+    float lo = value_of<BF>(ends & 0xFFFF);
+    const float hi = -value_of<BF>(ends >> 16);
+    const unsigned group_lanes = ((1u << LANES) - 1u) << (lane & ~(LANES - 1));
     bool bad = (__ballot_sync(kFull, (odd & 0x80008000u) != 0) & group_lanes) != 0;
     if (__any_sync(kFull, lo == 0.f)) {
         // a zero's sign: the first of the group's zeros in order
         float z = 1.f;
 #pragma unroll
-        for (int j = 7; j >= 0; --j) z = v[j] == 0.f ? v[j] : z;
+        for (int j = 4 * NW - 1; j >= 0; --j) {
+            const float v1 = value_of<BF>(raw[j] >> 16), v0 = value_of<BF>(raw[j] & 0xFFFF);
+            z = v1 == 0.f ? v1 : z;
+            z = v0 == 0.f ? v0 : z;
+        }
         const unsigned with = __ballot_sync(kFull, z == 0.f) & group_lanes;
         z = __shfl_sync(kFull, z, with ? __ffs(with) - 1 : lane);
         if (lo == 0.f) lo = z;
@@ -112,53 +145,71 @@ __device__ __forceinline__ Quantized quantize_word(uint4 u, int is_bf16) {
     bad |= (r.s & 0x7C00) == 0x7C00 || (r.b & 0x7C00) == 0x7C00;
     if (bad) r.s = r.b = 0x7FFF;
     const float s = __half2float(__ushort_as_half(r.s)), bf = __half2float(__ushort_as_half(r.b));
-    r.word = 0;
+    r.w[0] = r.w[1] = 0;
     if (!bad && s != 0.f) {
-        // rint(RN(d / s)) from t = d * RN(1 / s), which is within 2^-22 of d / s in relative terms (two
-        // roundings): clamped to [0, 15] it has the same nearest whole number unless it lies within 2^-12 of
-        // a half; where one of the eight does, the divisions themselves decide
+        // rint(RN(d / s)) from t = d * RN(1 / s), which is within 2^-22 of d / s in relative terms: it has the
+        // same nearest whole number unless it lies within 2^-12 of a half.  No code leaves [0, 15] where the
+        // bias is off by less than 0.4 s (fp16's half step, 2^-11 of it or 2^-25), as the scale's own rounding
+        // moves the last code by 15 * 2^-11.  Elsewhere the divisions themselves decide.
         const float inv = __frcp_rn(s);
         constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-        float off = 0.f;
+        const uint64_t nb = pack2(-bf, -bf), inv2 = pack2(inv, inv), whole = pack2(kWhole, kWhole), nwhole = pack2(-kWhole, -kWhole);
+        const uint64_t ninv2 = pack2(-inv, -inv);
+        float off = fmaxf(fabsf(bf) * 0x1p-11f, 0x1p-25f) > 0.4f * s ? 1.f : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float t = fminf(fmaxf(__fsub_rn(v[j], bf) * inv, 0.f), 15.f), w = __fadd_rn(t, kWhole);
-            off = fmaxf(off, fabsf(t - __fsub_rn(w, kWhole)));
-            r.word |= (__float_as_uint(w) & 15u) << (4 * j);
+        for (int k = 0; k < NW; ++k) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+                const uint32_t h = raw[4 * k + j];
+                const uint64_t v = BF ? pack2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u))
+                                      : pack2(value_of<false>(h & 0xFFFF), value_of<false>(h >> 16));
+                const uint64_t d = add_f32x2(v, nb), w = fma_f32x2(d, inv2, whole);
+                const float2 e = unpack2(fma_f32x2(d, ninv2, add_f32x2(w, nwhole)));  // whole number - t
+                const float2 q = unpack2(w);
+                off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
+                word = word * 16 + __float_as_uint(q.y);
+                word = word * 16 + __float_as_uint(q.x);
+            }
+            // each addend was 0x4B400000 + code: the constants' sum, 0x4B400000 * 0x11111111, comes off again
+            r.w[k] = word - 0x4B400000u * 0x11111111u;
         }
         if (off > 0.5f - 0.000244140625f) {
-            r.word = 0;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                r.w[k] = 0;
 #pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t h = (raw[j >> 1] >> (16 * (j & 1))) & 0xFFFF;
-                const float x = is_bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(uint16_t(h)));
-                r.word |= uint32_t(clamp_int(__float2int_rn(__fdiv_rn(__fsub_rn(x, bf), s)), 0, 15)) << (4 * j);
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t two = j < 2 ? raw[4 * k] : j < 4 ? raw[4 * k + 1] : j < 6 ? raw[4 * k + 2] : raw[4 * k + 3];
+                    const float x = value_of<BF>((two >> (16 * (j & 1))) & 0xFFFF);
+                    r.w[k] |= uint32_t(clamp_int(__float2int_rn(__fdiv_rn(__fsub_rn(x, bf), s)), 0, 15)) << (4 * j);
+                }
             }
         }
     }
     return r;
 }
 
-template <int GRP>
+template <int GRP, bool BF, int NW>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ KvArgs a) {
     grid_dependency_wait();
     grid_dependents_launch();
-    const Word w = my_word(a);
-    const uint16_t* ksrc = a.k + int64_t(w.tok) * a.k_ts + int64_t(w.h) * a.k_hs + w.p8 * 8;
-    const uint16_t* vsrc = a.v + int64_t(w.tok) * a.v_ts + int64_t(w.h) * a.v_hs + w.p8 * 8;
-    uint4 kraw, vraw;
-    if (a.vec) {
-        kraw = ldg_stream_v4(ksrc);
-        vraw = ldg_stream_v4(vsrc);
-    } else {
-        auto load = [](const uint16_t* p) {
-            uint32_t u[4];
+    const Words w = my_words<NW>(a);
+    const uint16_t* src[2] = {a.k + int64_t(w.tok) * a.k_ts + int64_t(w.h) * a.k_hs + w.at,
+                              a.v + int64_t(w.tok) * a.v_ts + int64_t(w.h) * a.v_hs + w.at};
+    uint32_t raw[2][4 * NW];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = uint32_t(p[2 * j]) | uint32_t(p[2 * j + 1]) << 16;
-            return make_uint4(u[0], u[1], u[2], u[3]);
-        };
-        kraw = load(ksrc);
-        vraw = load(vsrc);
+    for (int k = 0; k < 2; ++k) {
+        if (a.vec) {
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                const uint4 u = ldg_stream_v4(src[k] + 8 * j);
+                raw[k][4 * j] = u.x, raw[k][4 * j + 1] = u.y, raw[k][4 * j + 2] = u.z, raw[k][4 * j + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4 * NW; ++j) raw[k][j] = uint32_t(src[k][2 * j]) | uint32_t(src[k][2 * j + 1]) << 16;
+        }
     }
     const int b = seq_of(a.cu, a.seqs, w.tok);
     int64_t at = -1;
@@ -167,13 +218,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         at = cache_row(a, b, s.start + (w.tok - s.row0), w.h);
         flag_bad(at < 0);
     }
-    const Quantized k = quantize_word<GRP>(kraw, a.is_bf16), v = quantize_word<GRP>(vraw, a.is_bf16);
+    const Quantized k = quantize_words<GRP, BF, NW>(raw[0]), v = quantize_words<GRP, BF, NW>(raw[1]);
     if (at < 0) return;
-    const int64_t word = at * (a.dim / 8) + w.p8;
-    a.kc[word] = k.word;
-    a.vc[word] = v.word;
-    if (w.p8 % (GRP / 8) == 0) {
-        const int64_t gi = word / (GRP / 8);
+    const int64_t val = at * a.dim + w.at;
+    if constexpr (NW == 2) {
+        *reinterpret_cast<uint2*>(a.kc + val / 8) = make_uint2(k.w[0], k.w[1]);
+        *reinterpret_cast<uint2*>(a.vc + val / 8) = make_uint2(v.w[0], v.w[1]);
+    } else {
+        a.kc[val / 8] = k.w[0];
+        a.vc[val / 8] = v.w[0];
+    }
+    if (w.at % GRP == 0) {
+        const int64_t gi = val / GRP;
         a.ks[gi] = k.s, a.kb[gi] = k.b;
         a.vs[gi] = v.s, a.vb[gi] = v.b;
     }
@@ -201,7 +257,7 @@ __device__ __forceinline__ uint4 dequantize_word(uint32_t word, uint16_t sh, uin
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ KvArgs a) {
     grid_dependency_wait();
     grid_dependents_launch();
-    const Word w = my_word(a);
+    const Words w = my_words<1>(a);
     const int b = seq_of(a.cu, a.seqs, w.tok);
     if (!w.on || b >= a.seqs) return;
     const int c0 = clamp_int(a.cu[b], 0, a.tokens);
@@ -209,16 +265,16 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     const int64_t at = cache_row(a, b, a.at[b] + (w.tok - c0), w.h);
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     if (at >= 0) {
-        const int64_t word = at * (a.dim / 8) + w.p8;
-        const int64_t gi = a.group == 32 ? word >> 2 : a.group == 64 ? word >> 3 : word >> 4;
-        const uint32_t kw = a.kc[word], vw = a.vc[word];
+        const int64_t val = at * a.dim + w.at;
+        const int64_t gi = a.group == 32 ? val >> 5 : a.group == 64 ? val >> 6 : val >> 7;
+        const uint32_t kw = a.kc[val >> 3], vw = a.vc[val >> 3];
         const uint16_t ks = a.ks[gi], kb = a.kb[gi], vs = a.vs[gi], vb = a.vb[gi];
         k = dequantize_word(kw, ks, kb, a.is_bf16);
         v = dequantize_word(vw, vs, vb, a.is_bf16);
     }
     flag_bad(at < 0);
-    *reinterpret_cast<uint4*>(a.k_out + int64_t(w.tok) * a.k_ts + int64_t(w.h) * a.k_hs + w.p8 * 8) = k;
-    *reinterpret_cast<uint4*>(a.v_out + int64_t(w.tok) * a.v_ts + int64_t(w.h) * a.v_hs + w.p8 * 8) = v;
+    *reinterpret_cast<uint4*>(a.k_out + int64_t(w.tok) * a.k_ts + int64_t(w.h) * a.k_hs + w.at) = k;
+    *reinterpret_cast<uint4*>(a.v_out + int64_t(w.tok) * a.v_ts + int64_t(w.h) * a.v_hs + w.at) = v;
 }
 
 // ---------------------------------------------------------------- copy pages
@@ -342,21 +398,28 @@ cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t stream, cudaLaunc
     return cfg;
 }
 
-unsigned word_blocks(const KvArgs& a) {
-    return unsigned((int64_t(a.tokens) * a.kv_heads * (a.dim / 8) + kThreads - 1) / kThreads);
+unsigned word_blocks(const KvArgs& a, int words) {
+    return unsigned((int64_t(a.tokens) * a.kv_heads * (a.dim / (8 * words)) + kThreads - 1) / kThreads);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t stream) {
+template <int NW>
+cudaError_t append_words(const KvArgs& a, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a)), kThreads, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, a.group == 32 ? append_kernel<32> : a.group == 64 ? append_kernel<64> : append_kernel<128>, a);
+    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a, NW)), kThreads, stream, &attr);
+    auto fn = a.is_bf16 ? (a.group == 32 ? append_kernel<32, true, NW> : a.group == 64 ? append_kernel<64, true, NW> : append_kernel<128, true, NW>)
+                        : (a.group == 32 ? append_kernel<32, false, NW> : a.group == 64 ? append_kernel<64, false, NW> : append_kernel<128, false, NW>);
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+cudaError_t launch_kv_append(const KvArgs& a, cudaStream_t stream) {
+    return word_blocks(a, 1) > 148 * 8 ? append_words<2>(a, stream) : append_words<1>(a, stream);
 }
 
 cudaError_t launch_kv_gather(const KvArgs& a, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a)), kThreads, stream, &attr);
+    const cudaLaunchConfig_t cfg = config(dim3(word_blocks(a, 1)), kThreads, stream, &attr);
     return cudaLaunchKernelEx(&cfg, gather_kernel, a);
 }
 

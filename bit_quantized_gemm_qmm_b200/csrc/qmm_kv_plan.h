@@ -63,26 +63,25 @@ QMM_HD int attn_seq_units(const AttnSeq& s, int kv_heads) { return attn_seq_item
 
 QMM_HD int ceil_div_int(int a, int b) { return (a - 1) / b + 1; }  // a >= 1
 
-// How the work is dealt out over `blocks` blocks.  To begin an item costs a block about as much as
-// kAttnChange positions (its query rows, its sums and their join), so an item weighs its units and that.
+// How the work is dealt out over `blocks` blocks.  To begin an item costs a block about as much as `start`
+// units (its query rows, its sums and their join), so an item weighs its units and that.
 // Even shares: block i takes places [i * per, (i + 1) * per) of all items' weights, laid end to end, each
 // item's start before its units.  Pieces, where items are few: each item is cut into pieces of `per` units
 // (the last one shorter), one a block, so that no block changes items; the pieces are as small as keeps
 // their number within the blocks, and give each of a block's warps a unit at least.
-constexpr int kAttnChange = 384;
 struct AttnPlan {
     int total, per, pieces, start;  // weight of all; weight a block (units, in pieces); 1: pieces; an item's start
 };
-QMM_HD AttnPlan attn_plan(int units, int items, int blocks, int unit, int warps) {
+QMM_HD AttnPlan attn_plan(int units, int items, int blocks, int start, int warps) {
     AttnPlan p;
-    p.start = kAttnChange / unit;
+    p.start = start;
     p.total = units + items * p.start;
     p.pieces = 0;
     p.per = p.total < 1 ? 1 : ceil_div_int(p.total, blocks);
     if (units > 0 && items < blocks) {
         int piece = ceil_div_int(units, blocks - items);
         if (piece < warps) piece = warps;
-        if (piece <= p.per) p.pieces = 1, p.per = piece;
+        if (piece <= p.per + p.start / 2) p.pieces = 1, p.per = piece;
     }
     return p;
 }

@@ -19,7 +19,7 @@ HARNESS = r"""
 using namespace qmm_impl;
 // Walks the blocks as the kernels do.  Returns 0, or the number of the first check that fails.
 extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int capacity, int kv_heads, int gh, int rows,
-                    int window, int tree, int blocks, int unit, int warps) {
+                    int window, int tree, int blocks, int unit, int warps, int start) {
     std::vector<AttnSeq> s;
     std::vector<int> item0, unit0;  // items and units in front of each sequence
     int units = 0, items = 0;
@@ -33,7 +33,7 @@ extern "C" int walk(int seqs, const int* cu, const int* lens, int tokens, int ca
         units += attn_seq_units(q, kv_heads);
         items += attn_seq_items(q, kv_heads);
     }
-    const AttnPlan p = attn_plan(units, items, blocks, unit, warps);
+    const AttnPlan p = attn_plan(units, items, blocks, start, warps);
     if (p.per < 1) return 3;
     std::vector<int> taken(units, 0), slots(2 * blocks, -1);  // slot -> item
     struct Shared { int c0, c1; };
@@ -138,7 +138,7 @@ def test_every_unit_once_and_every_slot_its_own(walk):
         tree = 0 if window else rng.choice([0, 1])
         arr = lambda v: (ctypes.c_int * len(v))(*v)  # noqa: E731
         args = (seqs, arr(cu), arr(lens), tokens, page_cap, rng.choice([1, 2, 8]), rng.choice([1, 3, 4, 8]),
-                rng.choice([8, 16, 32, 64]), window, tree, rng.choice([1, 2, 7, 148, 296]), *rng.choice([(32, 4), (32, 6), (128, 1)]))
+                rng.choice([8, 16, 32, 64]), window, tree, rng.choice([1, 2, 7, 148, 296]), *rng.choice([(32, 4, 20), (32, 6, 20), (128, 1, 2), (32, 6, 0)]))
         got = walk(*args)
         assert got == 0, (got, seqs, cu, lens, args[3:])
 
