@@ -30,7 +30,7 @@
 // Work: units of 32 positions of one (sequence, K/V head, row tile) are dealt out evenly over
 // the resident blocks (qmm_kv_plan.h), whatever the lengths; a block's warps take them in turn, each
 // through its own cp.async ring.  Items that several blocks share are summed by the last of them to
-// arrive, in block order, so results do not depend on timing.
+// arrive, in an order that does not depend on timing.
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>
@@ -97,7 +97,7 @@ __device__ __forceinline__ void lds_halves(uint32_t addr, float (&f)[NG]) {
 // hold the warp's partial sums at the end of an item), then Q as MMA fragments and the rows' constants.
 template <int D, int GRP, int NT>
 struct AttnFmt {
-    static constexpr int W = D == 256 || NT > 2 ? 4 : 6;  // warps a block; two blocks an SM
+    static constexpr int W = 4, BLOCKS = D == 256 || NT > 1 ? 2 : 3;  // warps a block, blocks an SM
     static constexpr int NG = D / GRP;
     static constexpr int CH = D / 32;                 // 16-byte pieces (32 codes) of a row
     static constexpr int ROWS = 8 * NT;
@@ -109,8 +109,8 @@ struct AttnFmt {
     static constexpr int MS = (MERGE + TILE - 1) / TILE;  // ring slots under the partial sums
     static constexpr int QF = ROWS * D * 2;           // Q fragments
     static constexpr int CONSTS = ROWS * (4 + 4 + 8 + 8 * NG) + 16 + 3 * 96;
-    // the ring: four tiles, or as many as leave room for two blocks an SM
-    static constexpr int ROOM = 113 * 1024 - QF - CONSTS;
+    // the ring: four tiles, or as many as leave room for the SM's other blocks
+    static constexpr int ROOM = (BLOCKS == 2 ? 113 : 75) * 1024 - QF - CONSTS;
     static constexpr int FIT = ROOM / (W * TILE);
     static constexpr int RING = FIT > 4 ? 4 : FIT;
     static_assert(RING >= 2 && RING >= MS, "ring too small");
@@ -129,7 +129,7 @@ struct AttnFmt {
 };
 
 template <int D, int GRP, int NT>
-__global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, NT>::BLOCKS) attn_kernel(const __grid_constant__ AttnArgs a) {
     using F = AttnFmt<D, GRP, NT>;
     constexpr int NG = F::NG, CH = F::CH, R = F::ROWS, W = F::W, SUBS = F::SUBS, THREADS = 32 * W;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -689,18 +689,19 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, 2) attn_kernel(co
 using AttnFn = void (*)(const AttnArgs);
 struct AttnInst {
     AttnFn fn;
-    int smem, slot, rows, threads;
+    int smem, slot, rows, threads, blocks;
 };
 
 template <int D, int GRP, int NT>
 AttnInst inst() {
     using F = AttnFmt<D, GRP, NT>;
-    static_assert(F::SMEM <= 114 * 1024, "two blocks do not fit an SM");
-    return AttnInst{attn_kernel<D, GRP, NT>, F::SMEM, F::SLOT, F::ROWS, 32 * F::W};
+    static_assert(F::SMEM <= (F::BLOCKS == 2 ? 114 : 76) * 1024, "the blocks do not fit an SM");
+    return AttnInst{attn_kernel<D, GRP, NT>, F::SMEM, F::SLOT, F::ROWS, 32 * F::W, F::BLOCKS};
 }
 template <int D, int GRP>
 AttnInst inst_nt(int nt) {
-    return nt == 1 ? inst<D, GRP, 1>() : inst<D, GRP, 2>();
+    if constexpr (D == 256) return nt == 1 ? inst<D, GRP, 1>() : inst<D, GRP, 2>();
+    else return nt == 1 ? inst<D, GRP, 1>() : nt == 2 ? inst<D, GRP, 2>() : nt == 3 ? inst<D, GRP, 3>() : inst<D, GRP, 4>();
 }
 AttnInst instance(int d, int grp, int nt) {
     if (d == 64) return grp == 32 ? inst_nt<64, 32>(nt) : inst_nt<64, 64>(nt);
@@ -740,9 +741,9 @@ cudaError_t attn_blocks(void (*fn)(const AttnArgs), int smem, int per_sm, int re
 }
 
 cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threads, int smem, int slot, int rows, int unit,
-                               int regs, cudaStream_t stream) {
+                               int per_sm, int regs, cudaStream_t stream) {
     int blocks = 0;
-    cudaError_t e = attn_blocks(fn, smem, 2, regs, &blocks);  // both kernels are built for two blocks an SM
+    cudaError_t e = attn_blocks(fn, smem, per_sm, regs, &blocks);
     if (e != cudaSuccess) return e;
     // never more blocks than units there can be
     const int64_t tiles = int64_t(a.tokens) * a.group_heads / rows + a.seqs;
@@ -750,7 +751,7 @@ cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threa
     const int64_t units = tiles * a.kv_heads * (per_item > 0 ? per_item : 1);
     if (units >= int64_t(1) << 30) return cudaErrorNotSupported;
     if (units < blocks) blocks = int(units);
-    if (blocks > kArrivalCounters) blocks = kArrivalCounters;
+    if (blocks > kArrivalBlocks) blocks = kArrivalBlocks;
     void* ws = nullptr;
     e = split_workspace(stream, size_t(2) * blocks * slot * sizeof(float), &ws);
     if (e != cudaSuccess) return e;
@@ -776,9 +777,13 @@ cudaError_t launch_attn(const AttnArgs& a, int head_dim, int group, cudaStream_t
     // taken to have half as many again (columns that a tile does not fill cost next to nothing)
     const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
     const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
-    if (rows > 8 && attn_tc_supported(head_dim)) return launch_attn_tc(a, head_dim, group, rows, stream);
-    const AttnInst k = instance(head_dim, group, rows <= 8 ? 1 : 2);
-    return launch_attn_blocks(a, k.fn, k.threads, k.smem, k.slot, k.rows, kAttnUnit, 0, stream);
+    // up to 32 rows (four columns) the warps' kernel is faster (8 sequences of 6 tokens of 4 heads over 16k
+    // positions: 53 us against 68), above them the tensor-core kernel, which takes 64 rows at a time (4 of 16
+    // tokens over 8k: 62 against 72); heads of 256 have two columns of the former only
+    if (rows > 32 && attn_tc_supported(head_dim)) return launch_attn_tc(a, head_dim, group, stream);
+    const int64_t cols = (rows + 7) / 8, most = head_dim == 256 ? 2 : 4;
+    const AttnInst k = instance(head_dim, group, int(cols < most ? cols : most));
+    return launch_attn_blocks(a, k.fn, k.threads, k.smem, k.slot, k.rows, kAttnUnit, k.blocks, 0, stream);
 }
 
 cudaError_t attn_read_and_clear_errors(unsigned* out) {

@@ -165,49 +165,77 @@ __device__ __forceinline__ int plan_block(const AttnArgs& a, AttnCut cut, int la
     return b < a.seqs && plan_run(a, *pl, cut, x, *x_end, b, before, writer, r, bad) ? 1 : 0;
 }
 
-// Counts this block's sums of an item in (all of the block's threads call it, with its sums written);
-// the last of the item's blocks to arrive adds them in block order and writes the rows.  A slot is
-// [ROWS][D] sums, the rows' references and their l.
+// Joins the sums of an item that several blocks share (all of a block's threads call it, with its own sums
+// written to its slot).  Eight neighbouring blocks' sums are added by the last of them to arrive, eight such
+// results by the last of those, and so on: always in block order, and each step reads its slots in one
+// round (55 blocks of a 128k-position sequence: 2 steps; one block adding all of them took 7 rounds).  A
+// slot is [ROWS][D] sums, the rows' references and their l; a step's result goes to its first block's.
 template <int D, int ROWS>
 __device__ __forceinline__ void join_item(const AttnArgs& a, const Run* cur, int tid, int threads, int* flag) {
-    const int c0 = cur->c0, c1 = cur->c1;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) *flag = atomicInc(a.count + c0, unsigned(c1 - c0)) == unsigned(c1 - c0);  // wraps to 0
-    __syncthreads();
-    if (!*flag) return;
-    __threadfence();
-    auto slot_of = [&](int i) { return a.part + int64_t(attn_slot(i, c0)) * (ROWS * (D + 2)); };
-    for (int i = tid; i < cur->rows * (D / 4); i += threads) {
-        const int row = i / (D / 4), d = i % (D / 4) * 4;
-        float top = kNoRef, lsum = 0.f;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q0 = c0; q0 <= c1; q0 += 8) {
-            float4 v[8];
-            float rf[8], ll[8], now = top;
+    const int c0 = cur->c0, n = cur->c1 - c0 + 1;
+    int me = int(blockIdx.x) - c0;
+    auto slot_of = [&](int i) { return a.part + int64_t(attn_slot(c0 + i, c0)) * (ROWS * (D + 2)); };
+    for (int span = 1, level = 0;; span *= 8, ++level) {
+        me -= me % (8 * span);  // the first of the eight
+        const int left = (n - me + span - 1) / span, members = left < 8 ? left : 8;
+        if (members > 1) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0)  // wraps to 0
+                *flag = atomicInc(a.count + level * kArrivalBlocks + c0 + me, unsigned(members - 1)) == unsigned(members - 1);
+            __syncthreads();
+            if (!*flag) return;
+            __threadfence();
+        }
+        const bool last = 8 * span >= n;
+        if (members > 1 || last) {
+            for (int i = tid; i < cur->rows * (D / 4); i += threads) {
+                const int row = i / (D / 4), d = i % (D / 4) * 4;
+                float4 v[8];
+                float rf[8], ll[8], top = kNoRef;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const bool on = q0 + k <= c1;
-                const float* from = slot_of(on ? q0 + k : c1);
-                rf[k] = on ? __ldcg(from + ROWS * D + row) : kNoRef;
-                ll[k] = on ? __ldcg(from + ROWS * D + ROWS + row) : 0.f;
-                v[k] = on ? __ldcg(reinterpret_cast<const float4*>(from + row * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+                for (int k = 0; k < 8; ++k) {
+                    const bool on = k < members;
+                    const float* from = slot_of(on ? me + k * span : me);
+                    rf[k] = on ? __ldcg(from + ROWS * D + row) : kNoRef;
+                    ll[k] = on ? __ldcg(from + ROWS * D + ROWS + row) : 0.f;
+                    v[k] = on ? __ldcg(reinterpret_cast<const float4*>(from + row * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) now = fmaxf(now, rf[k]);
-            const float f0 = ex2(top - now);
-            sum.x *= f0, sum.y *= f0, sum.z *= f0, sum.w *= f0, lsum *= f0;
-            top = now;
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, rf[k]);
+                float lsum = 0.f;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float f = ex2(rf[k] - top);
-                sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
-                sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
-                lsum = fmaf(f, ll[k], lsum);
+                for (int k = 0; k < 8; ++k) {
+                    const float f = ex2(rf[k] - top);
+                    sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
+                    sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
+                    lsum = fmaf(f, ll[k], lsum);
+                }
+                if (last) {
+                    const int qr = cur->row_lo + row, tok = qr / a.group_heads;
+                    store_row4(a, cur->row0 + tok, cur->h * a.group_heads + qr - tok * a.group_heads, d, sum, lsum, top);
+                } else {
+                    __stcg(reinterpret_cast<float4*>(slot_of(me) + row * D + d), sum);
+                }
             }
         }
-        const int qr = cur->row_lo + row, tok = qr / a.group_heads;
-        store_row4(a, cur->row0 + tok, cur->h * a.group_heads + qr - tok * a.group_heads, d, sum, lsum, top);
+        if (last) return;
+        if (members > 1) {  // the rows' constants, once nobody reads the old ones
+            __syncthreads();
+            for (int row = tid; row < cur->rows; row += threads) {
+                float rf[8], top = kNoRef, lsum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) rf[k] = k < members ? __ldcg(slot_of(me + k * span) + ROWS * D + row) : kNoRef;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, rf[k]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < members) lsum = fmaf(ex2(rf[k] - top), __ldcg(slot_of(me + k * span) + ROWS * D + ROWS + row), lsum);
+                __stcg(slot_of(me) + ROWS * D + row, top);
+                __stcg(slot_of(me) + ROWS * D + ROWS + row, lsum);
+            }
+        }
     }
 }
 
@@ -216,10 +244,10 @@ __device__ __forceinline__ void join_item(const AttnArgs& a, const Run* cur, int
 cudaError_t attn_blocks(void (*fn)(const AttnArgs), int smem, int per_sm, int regs, int* out);
 // Launches a kernel over the resident blocks, with its workspace.
 cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threads, int smem, int slot, int rows, int unit,
-                               int regs, cudaStream_t stream);
-// The tensor-core kernel (qmm_attn_tc.cu); rows: query rows of the longer sequences.
+                               int per_sm, int regs, cudaStream_t stream);
+// The tensor-core kernel (qmm_attn_tc.cu).
 bool attn_tc_supported(int head_dim);
-cudaError_t launch_attn_tc(const AttnArgs& a, int head_dim, int group, int64_t rows, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnArgs& a, int head_dim, int group, cudaStream_t stream);
 cudaError_t attn_tc_read_and_clear_errors(unsigned* out);
 
 }  // namespace qmm_impl

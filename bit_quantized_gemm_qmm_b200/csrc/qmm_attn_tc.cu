@@ -658,25 +658,24 @@ TcAttnInst inst() {
     using F = TcAttnFmt<D, GRP, N>;
     return TcAttnInst{attn_tc_kernel<D, GRP, N>, F::SMEM, F::SLOT, N};
 }
+// 64 rows at a time, where P goes in one term and the groups' columns leave room; else 32
 template <int D, int GRP>
-TcAttnInst inst_n(int n) {
-    if constexpr (D / GRP > 2) return n == 16 ? inst<D, GRP, 16>() : inst<D, GRP, 32>();
-    else return n == 16 ? inst<D, GRP, 16>() : n == 32 ? inst<D, GRP, 32>() : inst<D, GRP, 64>();
+TcAttnInst inst_n(bool bf16) {
+    if constexpr (D / GRP > 2) return inst<D, GRP, 32>();
+    else return bf16 ? inst<D, GRP, 64>() : inst<D, GRP, 32>();
 }
-TcAttnInst instance(int d, int grp, int n) {
-    if (d == 64) return grp == 32 ? inst_n<64, 32>(n) : inst_n<64, 64>(n);
-    return grp == 32 ? inst_n<128, 32>(n) : grp == 64 ? inst_n<128, 64>(n) : inst_n<128, 128>(n);
+TcAttnInst instance(int d, int grp, bool bf16) {
+    if (d == 64) return grp == 32 ? inst_n<64, 32>(bf16) : inst_n<64, 64>(bf16);
+    return grp == 32 ? inst_n<128, 32>(bf16) : grp == 64 ? inst_n<128, 64>(bf16) : inst_n<128, 128>(bf16);
 }
 
 }  // namespace
 
 bool attn_tc_supported(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
-cudaError_t launch_attn_tc(const AttnArgs& in, int head_dim, int group, int64_t rows, cudaStream_t stream) {
-    AttnArgs a = in;
-    // 64 rows at a time only with P in one term
-    const TcAttnInst k = instance(head_dim, group, rows <= 16 ? 16 : rows <= 32 || !a.is_bf16 ? 32 : 64);
-    return launch_attn_blocks(a, k.fn, kTcThreads, k.smem, k.slot, k.rows, kAttnTcUnit, k.rows > 32 ? 128 : 0, stream);
+cudaError_t launch_attn_tc(const AttnArgs& a, int head_dim, int group, cudaStream_t stream) {
+    const TcAttnInst k = instance(head_dim, group, a.is_bf16 != 0);
+    return launch_attn_blocks(a, k.fn, kTcThreads, k.smem, k.slot, k.rows, kAttnTcUnit, 2, k.rows > 32 ? 128 : 0, stream);
 }
 
 cudaError_t attn_tc_read_and_clear_errors(unsigned* out) {

@@ -94,7 +94,8 @@ bool stream_supported(int64_t M, int64_t N, int64_t K, int bits, int group);
 cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out);
 // Arrival counters of a stream (and of each graph capture in progress on it), zero between calls:
 // whoever counts with them leaves them zero (atomicInc that wraps at the last arrival does).
-constexpr int kArrivalCounters = 4096;
+constexpr int kArrivalBlocks = 4096;                   // blocks of a launch at most
+constexpr int kArrivalCounters = 4 * kArrivalBlocks;  // joined by eights: a counter a block and step
 cudaError_t arrival_counters(cudaStream_t stream, unsigned** out);
 // A fresh 48-bit tag for the arrival words of one call (never 0).
 unsigned long long next_call_token();
