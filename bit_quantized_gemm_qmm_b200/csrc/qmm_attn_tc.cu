@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
     const int me = tid & (kPos - 1);     // this thread's position of a tile
     const bool softmax = tid < kPos;
     // full: scores of a tile are in tensor memory, K's place is free, and OFF_POS is written; free: the scores
-    // have been read; vfull: V is in place; done: O is up to date, V's and P's places are free
-    const uint32_t bar_full = sbase + F::OFF_BAR, bar_free = bar_full + 8, bar_vfull = bar_full + 16, bar_done = bar_full + 24;
+    // have been read; both: V and P are in place; done: O is up to date, V's and P's places are free
+    const uint32_t bar_full = sbase + F::OFF_BAR, bar_free = bar_full + 8, bar_both = bar_full + 16, bar_done = bar_full + 24;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + F::OFF_BAR + 32);
     int* const flag = reinterpret_cast<int*>(smem + F::OFF_BAR + 36);
 
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
     if (tid == 0) {
         mbar_init(bar_full, kPos + 1);
         mbar_init(bar_free, kPos);
-        mbar_init(bar_vfull, kPos);
+        mbar_init(bar_both, kTcThreads);
         mbar_init(bar_done, 1);
         fence_mbar_init();
     }
@@ -288,17 +288,19 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
         if constexpr (F::SPLIT) regs_down<kRegsC>();
         uint4 kr[WORDS / 4], vr[WORDS / 4];
         uint16_t ksr[NG], kbr[NG], vsr[NG], vbr[NG];
-        int page = -1;
+        int page = -1, in_page = 0;
         int64_t row = -1;  // of the cache, for the tile that is fetched; -1: not there
         auto look = [&](const Run* r, int u) {  // the page, a tile ahead of the rows
             const int t = r->t0 + kPos * u + me;
-            page = u < r->n && t < r->hi ? a.table[int64_t(r->b) * a.table_stride + t / a.page] : -1;
+            const int col = t / a.page;
+            in_page = t - col * a.page;
+            page = u < r->n && t < r->hi ? a.table[int64_t(r->b) * a.table_stride + col] : -1;
         };
         auto fetch_k = [&](const Run* r, int u) {
             const int t = r->t0 + kPos * u + me;
             const bool in = u < r->n && t < r->hi, there = in && page >= 0 && page < a.pages;
             bad |= in && !there;
-            row = there ? (int64_t(page) * a.kv_heads + r->h) * a.page + t % a.page : -1;
+            row = there ? (int64_t(page) * a.kv_heads + r->h) * a.page + in_page : -1;
             if (there) {
                 const uint4* k = reinterpret_cast<const uint4*>(a.kc + row * (D / 2));
 #pragma unroll
@@ -317,6 +319,21 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 for (int i = 0; i < WORDS / 4; ++i) vr[i] = __ldg(v + i);
             }
         };
+        // V^T P of tile number `of`: the first of its run overwrites O
+        auto sums = [&](uint32_t of, bool add) {
+            if (tid == kPos + 32) {
+                wait(bar_both, of);
+                tc_fence_after();
+                for (int term = 0; term < (N > 32 || a.is_bf16 ? 1 : 2); ++term)
+#pragma unroll
+                    for (int k = 0; k < kPos / 16; ++k)
+                        umma_f16_ss(tmem + F::COL_O, desc_sw128(sbase + F::OFF_V + k * 2048, F::PANEL, 1024),
+                                    desc_sw128(sbase + F::OFF_P + term * 64 + k * 2048, F::PANEL, 1024), idesc_t,
+                                    add || term || k);
+                umma_commit(bar_done);
+            }
+            __syncwarp();
+        };
         int u = seek(cur, 0);
         look(cur, u);
         fetch_k(cur, u);
@@ -325,6 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
         while (true) {
             stage_q();
             __syncthreads();
+            uint32_t in_run = 0;  // tiles of this run so far
             while (u < cur->n) {
                 const bool there = row >= 0;
                 const bool masked = !(cur->t0 + kPos * u >= cur->full_lo && cur->t0 + kPos * (u + 1) <= cur->full_hi);
@@ -377,7 +395,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                     fetch_k(cur, u_next);
                     look(cur, seek(cur, u_next + 1));
                 }
-                // ---- V
+                // ---- the last tile's sums (whose V is in the way), then V
+                if (in_run) sums(tile - 1, in_run > 1);
                 if (tile) wait(bar_done, tile - 1);
 #pragma unroll
                 for (int i = 0; i < WORDS; ++i) {
@@ -393,11 +412,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                     put(F::OFF_V, i, o);
                 }
                 fence_async_smem();
-                mbar_arrive(bar_vfull);
+                mbar_arrive(bar_both);
                 if (u_next < cur->n) fetch_v();
-                ++tile;
+                ++tile, ++in_run;
                 u = u_next;
             }
+            if (in_run) sums(tile - 1, in_run > 1);
             // ---- the next run's first rows are on their way while the softmax warps put this one together
             const bool more = plan_run(a, pl, cut, cur->x + cur->places, x_end, cur->b, cur->before, tid == kPos, next, &bad);
             group_sync(1);
@@ -573,19 +593,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 }
                 fence_async_smem();
                 tc_fence_before();
-                group_sync(2);
-                if (tid == 0) {
-                    wait(bar_vfull, tile);
-                    tc_fence_after();
-                    for (int term = 0; term < (N > 32 || a.is_bf16 ? 1 : 2); ++term)
-#pragma unroll
-                        for (int k = 0; k < kPos / 16; ++k)
-                            umma_f16_ss(tmem + F::COL_O, desc_sw128(sbase + F::OFF_V + k * 2048, F::PANEL, 1024),
-                                        desc_sw128(sbase + F::OFF_P + term * 64 + k * 2048, F::PANEL, 1024), idesc_t,
-                                        any_tile || term || k);
-                    umma_commit(bar_done);
-                }
-                __syncwarp();
+                mbar_arrive(bar_both);
                 any_tile = true;
                 ++tile;
                 u = seek(cur, u + 1);
