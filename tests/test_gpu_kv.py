@@ -100,6 +100,21 @@ ATTENTION = {
     "mqa": (128, 64, 64, 1, 32, BF, [700, 33], [1, 2], 0, False),
     "mha": (128, 64, 64, 16, 1, HF, [260, 33], [1, 1], 0, False),
     "long": (128, 64, 64, 2, 4, HF, [20000], [2], 0, False),
+    "long, one head": (64, 64, 64, 1, 1, BF, [100000], [1], 0, False),
+    "long and short": (128, 64, 64, 1, 16, HF, [30000, 3, 40, 9000], [1, 1, 1, 1], 0, False),
+    "32 rows": (128, 64, 64, 1, 4, BF, [900, 555], [8, 3], 0, False),
+    "24 rows dim 64": (64, 32, 32, 2, 4, HF, [900, 31], [6, 2], 0, False),
+    "33 rows": (128, 64, 64, 2, 33, BF, [700], [1], 0, False),
+    "many rows dim 128 group 128": (128, 128, 64, 2, 4, BF, [700, 129], [40, 70], 0, False),
+    "many rows dim 64 group 64": (64, 64, 16, 2, 8, BF, [257, 40], [40, 40], 0, False),
+    "many rows dim 64 group 32 fp16": (64, 32, 48, 2, 5, HF, [1000], [50], 0, False),
+    "many rows dim 128 group 128 fp16": (128, 128, 16, 1, 12, HF, [500, 77], [12, 30], 0, False),
+    "many rows dim 128 group 32": (128, 32, 64, 1, 8, BF, [640], [20], 0, False),
+    "many rows long": (128, 64, 64, 1, 8, BF, [40000], [9], 0, False),
+    "many rows, some empty": (128, 64, 64, 2, 4, BF, [0, 300, 10, 64], [20, 0, 30, 64], 0, False),
+    "many rows window 200": (128, 64, 64, 2, 4, BF, [1500, 130], [100, 130], 200, False),
+    "many rows tree": (128, 64, 64, 2, 4, BF, [400, 40], [64, 33], 0, True),
+    "dim 256 many rows": (256, 64, 16, 1, 8, BF, [300], [20], 0, False),
     "many short": (64, 64, 16, 2, 2, BF, [1 + (7 * i) % 23 for i in range(97)], [1] * 97, 0, False),
 }
 
@@ -158,9 +173,10 @@ def test_attention_leaves_rows_of_no_sequence():
         assert (t[:2] == 7).all() and (t[T + 2:] == 7).all()
 
 
-def test_attention_does_not_see_nan_and_infinity_behind_the_mask():
+@pytest.mark.parametrize("name", ["tree", "many rows tree", "tree of 64"])
+def test_attention_does_not_see_nan_and_infinity_behind_the_mask(name):
     """Draft rows that a token's tree mask or position hides may hold anything."""
-    c, x, table, lens, cu, scale, _, _ = attention_case("tree")
+    c, x, table, lens, cu, scale, _, _ = attention_case(name)
     T = x.shape[0]
     bits = torch.ones(T, dtype=torch.int64, device="cuda")  # everyone sees draft token 0 of its sequence only
     want = ref.attention(c.arrays(), c.page_size, x, table, lens.tolist(), cu.tolist(), scale, 0, bits)
@@ -193,16 +209,17 @@ def test_attention_nan_query_stays_in_its_row():
     check(o, lse, want)
 
 
+@pytest.mark.parametrize("new", [2, 40])
 @pytest.mark.parametrize("what", ["large V", "small V", "V of one value", "zero V", "loud late key", "rising keys", "small q",
                                   "large q", "mixed V"])
-def test_attention_ranges(what):
-    """Values far from one: the running references must follow them."""
+def test_attention_ranges(what, new):
+    """Values far from one: the running references must follow them (both kernels)."""
     dim, group, page, hk, grp = 128, 64, 64, 2, 4
     n, pages = 1500, 24
     c = q.KVCache.empty(pages, page, hk, dim, group)
     k = torch.randn((n, hk, dim), device="cuda", generator=gen(3))
     v = torch.randn((n, hk, dim), device="cuda", generator=gen(4))
-    x = torch.randn((2, hk * grp, dim), device="cuda", generator=gen(5))
+    x = torch.randn((new, hk * grp, dim), device="cuda", generator=gen(5))
     if what == "large V":
         v = v * 12000
     if what == "small V":
@@ -225,12 +242,30 @@ def test_attention_ranges(what):
     table = page_tables([n], page, pages, 6)
     lens = ints([n])
     q.kv_append(c, k, v, table, lens, ints([0, n]))
-    cu = ints([0, 2])
+    cu = ints([0, new])
     o, lse = q.kv_attention(c, x, table, lens, cu)
-    want = ref.attention(c.arrays(), page, x, table, [n], [0, 2], dim ** -0.5)
+    want = ref.attention(c.arrays(), page, x, table, [n], [0, new], dim ** -0.5)
     check(o, lse, want, what)
     if what == "zero V":
         assert (o == 0).all()
+
+
+def test_attention_bad_pages_many_rows():
+    """The same in the kernel for many rows: what a missing page would have held is left out."""
+    c, x, table, lens, cu, scale, _, _ = attention_case("many rows dim 128 group 128")
+    for bad in (-1, c.pages, -2 ** 31):
+        t2 = table.clone()
+        t2[0, 3] = bad  # positions 192..255 of the sequence of 700
+        o, lse = q.kv_attention(c, x, t2, lens, cu)
+        torch.cuda.synchronize()
+        assert q.device_errors() == 2
+        keep = [p for p in range(700) if not 192 <= p < 256]
+        (kc, ks, kb), (vc, vs, vb) = ref.rows_of(c.arrays(), table[0], keep, c.page_size)
+        last = 39  # sees all of them
+        s = torch.einsum("hd,htd->ht", x[last].double(), (ks * kc + kb).repeat_interleave(4, 0)) * scale
+        assert torch.allclose(lse[last].double(), torch.logsumexp(s, -1), atol=1e-4)
+        ok = ref.attention(c.arrays(), c.page_size, x, table, lens.tolist(), cu.tolist(), scale)
+        check(o[40:], lse[40:], [t[40:] for t in ok])
 
 
 def test_attention_bad_pages_and_lengths():
