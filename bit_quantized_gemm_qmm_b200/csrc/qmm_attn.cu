@@ -294,15 +294,15 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
             sts_v4(sbase + F::OFF_Q + ((nt * CH + ch) * 32 + ln) * 16, f);
             if (p8 % (GRP / 8) == 0) {
                 // the group's sum in the same units, as three fp16 terms
-                const float s0 = sum * 0x1p-24f, h0 = __half2float(__float2half_rn(s0));
+                const float s0 = sum * (0x1p-24f * kSumUp), h0 = __half2float(__float2half_rn(s0));
                 const float s1 = s0 - h0, h1 = __half2float(__float2half_rn(s1));
                 uint32_t* qb = reinterpret_cast<uint32_t*>(smem + F::OFF_QB + (row * NG + p8 / (GRP / 8)) * 8);
                 qb[0] = f32x2_to_f16x2(h0, h1);
                 qb[1] = f32x2_to_f16x2(s1 - h1, 0.f);
             }
             if (p8 == 0) {
-                // 2^24 * 2^-e in two exact steps (e may be as low as -113)
-                *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * 16777216.f * exp2i(-e);
+                // 2^24 / kSumUp * 2^-e in two steps (e may be as low as -113)
+                *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * (16777216.f / kSumUp) * exp2i(-e);
                 *reinterpret_cast<int*>(smem + F::OFF_LIM + row * 4) = row < cur->rows ? cur->start + tok : INT_MAX;
                 *reinterpret_cast<int64_t*>(smem + F::OFF_BITS + row * 8) =
                     a.tree != nullptr && row < cur->rows ? a.tree[cur->row0 + tok] : -1;
@@ -402,6 +402,8 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                 const uint32_t sb = st + 2 * F::CODES + (kAttnSub * (h0 + u) + g) * (2 * NG);
                 lds_halves<NG>(sb, ks[u][0]);
                 lds_halves<NG>(sb + 16 * NG, ks[u][1]);
+#pragma unroll
+                for (int j = 0; j < NG; ++j) ks[u][0][j] *= kSumUp, ks[u][1][j] *= kSumUp;
 #pragma unroll
                 for (int m = 0; m < QBM; ++m) {
                     const uint32_t at = sb + F::SB + (m * 4 + (NG < 4 ? c % NG : c)) * 2;

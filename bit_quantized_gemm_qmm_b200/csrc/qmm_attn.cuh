@@ -26,6 +26,11 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float half_lo(uint32_t v) { return __half2float(__ushort_as_half(uint16_t(v))); }
 __device__ __forceinline__ float half_hi(uint32_t v) { return __half2float(__ushort_as_half(uint16_t(v >> 16))); }
 
+// Score sums are in units of 2^-24 (codes are subnormal) times the row's power of two.  Sums of Q over a group
+// are raised by 2^17, and with them K's scales: up to 2^15 in fp16, so that three terms of 11 bits are all
+// normal numbers (without it the second would be subnormal, and the sum good to 2^-18 only).
+constexpr float kSumUp = 131072.f;
+
 // Four values of an output row: sum / l, rounded once; with the first of them the row's lse.
 // A row that saw nothing (l = 0) is zeros and -infinity.
 __device__ __forceinline__ void store_row4(const AttnArgs& a, int row, int head, int d, float4 v, float l, float ref) {

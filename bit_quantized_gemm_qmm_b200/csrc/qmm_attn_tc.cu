@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
             f.w = f32x2_to_f16x2(v[3] * 0.0625f, v[7] * 0.0625f);
             sts_v4(sbase + F::OFF_Q + place(row, p8, F::QPANEL), f);
             if (p8 % (GRP / 8) == 0) {
-                const float s0 = sum * 0x1p-24f, h0 = __half2float(__float2half_rn(s0));
+                const float s0 = sum * (0x1p-24f * kSumUp), h0 = __half2float(__float2half_rn(s0));
                 const float s1 = s0 - h0, h1 = __half2float(__float2half_rn(s1));
                 const float h[3] = {h0, h1, s1 - h1};
 #pragma unroll
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 }
             }
             if (p8 == 0) {
-                *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * 16777216.f * exp2i(-e);
+                *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * (16777216.f / kSumUp) * exp2i(-e);
                 *reinterpret_cast<float*>(smem + F::OFF_NREF + row * 4) = -kNoRef;
                 *reinterpret_cast<int*>(smem + F::OFF_LIM + row * 4) = row < cur->rows ? cur->start + tok : INT_MAX;
                 *reinterpret_cast<int64_t*>(smem + F::OFF_BITS + row * 8) =
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 uint32_t* const pos = reinterpret_cast<uint32_t*>(smem + F::OFF_POS) + (tile & 1) * kPos * (NG + 1) + me;
                 pos[NG * kPos] = (there ? 0u : kAbsent) | (odd ? kOdd : 0u);
 #pragma unroll
-                for (int j = 0; j < NG; ++j) pos[j * kPos] = __float_as_uint(__half2float(__ushort_as_half(ksr[j])));
+                for (int j = 0; j < NG; ++j) pos[j * kPos] = __float_as_uint(__half2float(__ushort_as_half(ksr[j])) * kSumUp);
                 fence_async_smem();
                 mbar_arrive(bar_full);
                 group_sync(1);

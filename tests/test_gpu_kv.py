@@ -146,6 +146,18 @@ def test_attention(name):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # the order of sums is fixed
 
 
+@pytest.mark.parametrize("name", ["one token", "ragged decodes", "dim 64 group 32 page 16", "dim 128 group 32 wide", "dim 256 group 32",
+                                  "64 draft tokens", "many rows dim 64 group 32 fp16", "many rows dim 128 group 128"])
+def test_attention_scores_are_fp32(name):
+    """As a whole the lse is as near as a plain fp32 computation's (whose dot products of up to 256 terms and
+    logarithm are some 2^-24 of their size off): a score that lost bits to 16-bit operands would be 2^-18 off."""
+    c, x, table, lens, cu, scale, window, bits = attention_case(name)
+    _, lse = q.kv_attention(c, x, table, lens, cu)
+    want = ref.attention(c.arrays(), c.page_size, x, table, lens.tolist(), cu.tolist(), scale)[1]
+    some = torch.isfinite(want)
+    assert (lse.double() - want)[some].norm() <= 2.0 ** -21 * want[some].norm()
+
+
 def test_attention_strides_scale_and_outputs():
     """q as a slice of a fused projection's output at an odd offset, o and lse given, another scale."""
     c, x, table, lens, cu, _, _, _ = attention_case("ragged decodes")
