@@ -58,7 +58,8 @@ struct TcAttnFmt {
     static constexpr int OFF_NREF = OFF_F + N * 4;
     static constexpr int OFF_LIM = OFF_F + N * 8;
     static constexpr int OFF_BITS = OFF_LIM + N * 4;
-    static constexpr int OFF_RED = OFF_BITS + N * 8;   // per warp and row
+    static constexpr int OFF_OUT = OFF_BITS + N * 8;   // per row: where its output is, in elements
+    static constexpr int OFF_RED = OFF_OUT + N * 8;    // per warp and row
     static constexpr int OFF_POS = OFF_RED + 4 * N * 4;    // per position, for two tiles: K's scales, what is the matter
     static constexpr int OFF_BAR = OFF_POS + 2 * kPos * (NG + 1) * 4;
     static constexpr int OFF_RUN = OFF_BAR + 64;       // this run and the next
@@ -222,20 +223,22 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
 
     // ---- Q of the current run: K-major panels, scaled by a power of two per row (as in qmm_attn.cu)
     auto stage_q = [&]() {
+        auto load = [&](int i) {
+            const int qr = cur->row_lo + i / WORDS, tok = qr / a.group_heads, hg = qr - tok * a.group_heads;
+            if (i / WORDS >= cur->rows) return make_uint4(0u, 0u, 0u, 0u);
+            const uint16_t* src = a.q + int64_t(cur->row0 + tok) * a.q_ts + int64_t(cur->h * a.group_heads + hg) * a.q_hs + i % WORDS * 8;
+            if (a.q_vec) return *reinterpret_cast<const uint4*>(src);
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = uint32_t(src[2 * j]) | uint32_t(src[2 * j + 1]) << 16;
+            return make_uint4(u[0], u[1], u[2], u[3]);
+        };
+        uint4 raw = load(tid);
+#pragma unroll 1
         for (int i = tid; i < N * WORDS; i += kTcThreads) {
             const int row = i / WORDS, p8 = i % WORDS;
-            const int qr = cur->row_lo + row, tok = qr / a.group_heads, hg = qr - tok * a.group_heads;
-            uint32_t rw[4] = {0, 0, 0, 0};
-            if (row < cur->rows) {
-                const uint16_t* src = a.q + int64_t(cur->row0 + tok) * a.q_ts + int64_t(cur->h * a.group_heads + hg) * a.q_hs + p8 * 8;
-                if (a.q_vec) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(src);
-                    rw[0] = x.x, rw[1] = x.y, rw[2] = x.z, rw[3] = x.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) rw[j] = uint32_t(src[2 * j]) | uint32_t(src[2 * j + 1]) << 16;
-                }
-            }
+            const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+            raw = load(i + kTcThreads);  // zeros past the last row
             float v[8];
             float mx = 0.f, sum = 0.f;
 #pragma unroll
@@ -273,6 +276,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 }
             }
             if (p8 == 0) {
+                const int qr = cur->row_lo + row, tok = qr / a.group_heads, head = cur->h * a.group_heads + qr - tok * a.group_heads;
+                *reinterpret_cast<int64_t*>(smem + F::OFF_OUT + row * 8) = int64_t(cur->row0 + tok) * a.o_ts + int64_t(head) * a.o_hs;
                 *reinterpret_cast<float*>(smem + F::OFF_F + row * 4) = a.scale_log2 * (16777216.f / kSumUp) * exp2i(-e);
                 *reinterpret_cast<float*>(smem + F::OFF_NREF + row * 4) = -kNoRef;
                 *reinterpret_cast<int*>(smem + F::OFF_LIM + row * 4) = row < cur->rows ? cur->start + tok : INT_MAX;
@@ -468,16 +473,22 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                         see = 0;
                         if (t < cur->keys) {
 #pragma unroll 1
-                            for (int r = 0; r < HR; ++r) {
-                                bool on;
+                            for (int r = 0; r < HR; r += 4) {
+                                uint32_t on = 0;
                                 if (a.tree != nullptr) {
-                                    const int64_t bits = *reinterpret_cast<const int64_t*>(smem + F::OFF_BITS + (h0 + r) * 8);
-                                    on = d < 0 || (d < 64 && ((bits >> d) & 1));
+                                    const uint4 b0 = lds_v4(sbase + F::OFF_BITS + (h0 + r) * 8), b1 = lds_v4(sbase + F::OFF_BITS + (h0 + r) * 8 + 16);
+                                    const uint32_t lo[4] = {b0.x, b0.z, b1.x, b1.z}, hi[4] = {b0.y, b0.w, b1.y, b1.w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        on |= (d < 0 ? 1u : d < 64 ? (d < 32 ? lo[k] >> d : hi[k] >> (d - 32)) & 1u : 0u) << k;
                                 } else {
-                                    const int lim = *reinterpret_cast<const int*>(smem + F::OFF_LIM + (h0 + r) * 4);
-                                    on = t <= lim && (a.window <= 0 || lim == INT_MAX || t > lim - a.window);
+                                    const uint4 l4 = lds_v4(sbase + F::OFF_LIM + (h0 + r) * 4);
+                                    const int lim[4] = {int(l4.x), int(l4.y), int(l4.z), int(l4.w)};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        on |= uint32_t(t <= lim[k] && (a.window <= 0 || lim[k] == INT_MAX || t > lim[k] - a.window)) << k;
                                 }
-                                see |= uint32_t(on) << r;
+                                see |= on << r;
                             }
                         }
                     }
@@ -610,6 +621,20 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
             tc_fence_after();
             const bool whole = cur->n == cur->units;
             float* const slot = a.part + int64_t(attn_slot(blockIdx.x, cur->c0)) * F::SLOT;
+            float* const inv = reinterpret_cast<float*>(smem + F::OFF_F);  // the factors are done with
+            if (tid < cur->rows) {
+                const float ls = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
+                inv[tid] = ls == 0.f ? 0.f : 1.f / ls;
+                if (!whole) {
+                    __stcg(slot + N * D + tid, -nref[tid]);
+                    __stcg(slot + N * D + N + tid, ls);
+                } else if (a.lse != nullptr) {
+                    const int qr = cur->row_lo + tid, tok = qr / a.group_heads;
+                    a.lse[int64_t(cur->row0 + tok) * (a.kv_heads * a.group_heads) + cur->h * a.group_heads + qr - tok * a.group_heads] =
+                        ls == 0.f ? -INFINITY : (lg2(ls) - nref[tid]) * 0.693147180559945309f;
+                }
+            }
+            group_sync(2);
             // this thread's d: the codes' order within a word
             const int o8 = me & 7, d = (me & ~7) + (o8 >> 1) + (o8 & 1) * 4;
 #pragma unroll 1
@@ -622,20 +647,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 for (int k = 0; k < CH; ++k) {
                     const int r = r0 + k;
                     if (r >= cur->rows || me >= D) continue;
-                    const float ls = (red[r] + red[N + r]) + (red[2 * N + r] + red[3 * N + r]);
                     const float v = any_tile ? __uint_as_float(o[k]) : 0.f;
                     if (whole) {
-                        const int qr = cur->row_lo + r, tok = qr / a.group_heads;
-                        const int head = cur->h * a.group_heads + qr - tok * a.group_heads;
-                        const float out = ls == 0.f ? 0.f : v / ls;
-                        uint16_t* dst = a.o + int64_t(cur->row0 + tok) * a.o_ts + int64_t(head) * a.o_hs + d;
-                        *dst = a.is_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(out)) : __half_as_ushort(__float2half_rn(out));
-                        if (me == 0 && a.lse != nullptr)
-                            a.lse[int64_t(cur->row0 + tok) * (a.kv_heads * a.group_heads) + head] =
-                                ls == 0.f ? -INFINITY : (lg2(ls) - nref[r]) * 0.693147180559945309f;
+                        const float out = v * inv[r];
+                        a.o[*reinterpret_cast<const int64_t*>(smem + F::OFF_OUT + r * 8) + d] =
+                            a.is_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(out)) : __half_as_ushort(__float2half_rn(out));
                     } else {
                         __stcg(slot + r * D + d, v);
-                        if (me == 0) __stcg(slot + N * D + r, -nref[r]), __stcg(slot + N * D + N + r, ls);
                     }
                 }
             }
