@@ -751,7 +751,7 @@ cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threa
     const int64_t tiles = int64_t(a.tokens) * a.group_heads / rows + a.seqs;
     const int64_t per_item = (int64_t(a.capacity) + unit - 1) / unit;
     const int64_t units = tiles * a.kv_heads * (per_item > 0 ? per_item : 1);
-    if (units >= int64_t(1) << 30) return cudaErrorNotSupported;
+    if (units >= int64_t(1) << 29) return cudaErrorNotSupported;  // with the items' starts, below 2^31
     if (units < blocks) blocks = int(units);
     if (blocks > kArrivalBlocks) blocks = kArrivalBlocks;
     void* ws = nullptr;

@@ -12,6 +12,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMaxTokens = int64_t(1) << 20;
 constexpr int64_t kMaxSeqs = 65536;
+constexpr int64_t kMaxPairs = 65536;  // every block looks through all of them
 constexpr int kMaxHeads = 256;
 
 qmm_status check_cache(const qmm_kv_cache* c) {
@@ -131,7 +132,7 @@ qmm_status qmm_kv_copy_pages(const qmm_kv_cache* cache, const int32_t* src, cons
     qmm_status s = check_cache(cache);
     if (s != QMM_OK) return s;
     if (pairs < 0) return fail(QMM_ERR_INVALID_ARG, "negative pairs=%lld", (long long)pairs);
-    if (pairs > kMaxTokens) return fail(QMM_ERR_UNSUPPORTED, "pairs=%lld > %lld", (long long)pairs, (long long)kMaxTokens);
+    if (pairs > kMaxPairs) return fail(QMM_ERR_UNSUPPORTED, "pairs=%lld > %lld", (long long)pairs, (long long)kMaxPairs);
     if (pairs == 0) return QMM_OK;
     if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4))
         return fail(QMM_ERR_INVALID_ARG, "src and dst must be 4-byte aligned pointers");
@@ -193,8 +194,12 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const void* q, int64_t q_
     a.scale_log2 = scale * 1.44269504088896341f;
     a.is_bf16 = dtype == QMM_BF16;
     a.q_vec = aligned(q, 16) && (q_token_stride | q_head_stride) % 8 == 0;
-    return launch_result(launch_attn(a, cache->head_dim, cache->group, static_cast<cudaStream_t>(stream)),
-                         "qmm_kv_attention launch");
+    try {  // the workspaces are kept in host containers
+        return launch_result(launch_attn(a, cache->head_dim, cache->group, static_cast<cudaStream_t>(stream)),
+                             "qmm_kv_attention launch");
+    } catch (...) {
+        return fail(QMM_ERR_CUDA, "qmm_kv_attention: out of host memory");
+    }
 }
 
 }  // extern "C"

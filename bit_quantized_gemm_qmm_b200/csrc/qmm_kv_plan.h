@@ -57,7 +57,7 @@ QMM_HD AttnSeq attn_seq(int c0, int c1, int len, int tokens, int capacity, int g
 
 // All units of a sequence: items (K/V head, row tile), row tiles next to one another, each of
 // s.units units of positions.  The host bounds the sum over all sequences (of offsets
-// that do not fall) below 2^30.
+// that do not fall) below 2^29, and there are at most 2^26 items.
 QMM_HD int attn_seq_items(const AttnSeq& s, int kv_heads) { return kv_heads * s.rt; }
 QMM_HD int attn_seq_units(const AttnSeq& s, int kv_heads) { return attn_seq_items(s, kv_heads) * s.units; }
 

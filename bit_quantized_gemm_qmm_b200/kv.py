@@ -67,7 +67,7 @@ class KVCache:
 
 
 _call = None
-_device = torch._C._cuda_getDevice
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _calls():

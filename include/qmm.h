@@ -339,7 +339,7 @@ qmm_status qmm_kv_gather(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, con
 
 /*
  * qmm_kv_copy_pages -- page dst[i] becomes a copy of page src[i], K and V, all heads, for i <
- * pairs (up to 2^20): the partly filled last page of a forked sequence, a pool that is made
+ * pairs (up to 65536): the partly filled last page of a forked sequence, a pool that is made
  * dense.  Of pairs with the same dst the last one counts.  A page must not be one pair's src and
  * another's dst: such a pair (the one that would read it) is skipped and sets bit 1 of
  * qmm_device_errors().
@@ -370,12 +370,16 @@ qmm_status qmm_kv_compact(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, co
  *          its sequence's new tokens and, of those, number j if bit j of its mask is set (those
  *          past 64 are not seen).  Not together with a window.
  * A row that sees nothing is zeros with lse = -infinity.  What a row does not see has no part
- * in it, NaN included.  Arithmetic: codes enter the tensor cores exactly; scores, softmax and sums
- * are fp32; each probability times V's scale is rounded once to fp16, q to fp16 relative to its
- * row's largest value (exact unless 2^-24 below it), o once.  Results do not depend on timing.
+ * in it, NaN included.  Arithmetic: K's codes enter the tensor cores exactly, q as fp16 relative to
+ * its row's largest value (exact unless 2^-24 below it); scores, softmax and sums are fp32; o is
+ * rounded once.  Up to 32 query rows a K/V head (new tokens times query heads; all of them at
+ * head_dim 256) V's codes are exact too and each probability times V's scale is rounded once to
+ * fp16; above, V is rounded to fp16 as qmm_dequantize does (|V| beyond 65504 there becomes infinity),
+ * and probabilities are fp16 for bf16 outputs and two fp16 terms for fp16 outputs.  Which of the
+ * two runs goes by tokens / seqs, not by the lengths.  Results do not depend on timing.
  * Uses the stream's workspace (as qmm), a captured call one of its capture: two instances of one
  * captured graph must not run at once.  The tiles of 8 query rows or more that the new tokens make,
- * times kv_heads, times max_pages * page_size / 32, must stay below 2^30.
+ * times kv_heads, times max_pages * page_size / 32, must stay below 2^29.
  */
 qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const void* q, int64_t q_token_stride,
                             int64_t q_head_stride, void* o, int64_t o_token_stride,

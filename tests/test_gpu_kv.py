@@ -173,8 +173,33 @@ def test_attention_strides_scale_and_outputs():
     assert (out[:, 0] == 7).all() and (out[:, T + 1] == 7).all()
 
 
-def test_attention_leaves_rows_of_no_sequence():
-    c, x, table, lens, cu, scale, _, _ = attention_case("ragged decodes")
+@pytest.mark.parametrize("name", ["many rows dim 128 group 128", "many rows dim 64 group 32 fp16", "32 rows"])
+def test_attention_strides_other_kernels(name):
+    c, x, table, lens, cu, scale, _, _ = attention_case(name)
+    T, H, D = x.shape
+    wide = torch.zeros((T, H * D + 17), dtype=x.dtype, device="cuda")
+    view = wide[:, 3: 3 + H * D].unflatten(1, (H, D))
+    view.copy_(x)
+    out = torch.full((H, T + 2, D), 7.0, dtype=x.dtype, device="cuda")
+    plain, lse = q.kv_attention(c, x, table, lens, cu)
+    _, lse2 = q.kv_attention(c, view.requires_grad_(False), table, lens, cu, out=out[:, 1: T + 1].transpose(0, 1))
+    assert torch.equal(out[:, 1: T + 1].transpose(0, 1), plain) and torch.equal(lse, lse2)
+    assert (out[:, 0] == 7).all() and (out[:, T + 1] == 7).all()
+    # without an lse, through the C ABI; and the call on a leaf that requires a gradient reads it as it is
+    import ctypes
+    o = torch.full_like(x, 7.0)
+    s = q.SeqsDesc(table.data_ptr(), cu.data_ptr(), table.shape[0], table.stride(0), table.shape[1])
+    st = q.lib().qmm_kv_attention(ctypes.byref(c._desc), x.data_ptr(), H * D, D, o.data_ptr(), H * D, D, None, ctypes.byref(s),
+                                  lens.data_ptr(), T, H, scale, 0, None, q.QMM_BF16 if x.dtype == BF else q.QMM_F16,
+                                  torch.cuda.current_stream().cuda_stream)
+    assert st == q.QMM_OK and torch.equal(o, plain)
+    leaf = x.detach().clone().requires_grad_(True)
+    assert torch.equal(q.kv_attention(c, leaf, table, lens, cu)[0].detach(), plain)
+
+
+@pytest.mark.parametrize("name", ["ragged decodes", "many rows dim 128 group 128"])
+def test_attention_leaves_rows_of_no_sequence(name):
+    c, x, table, lens, cu, scale, _, _ = attention_case(name)
     T, H, D = x.shape
     pad = torch.cat([x[:2], x, x[:3]])
     out, lse = torch.full((T + 5, H, D), 7.0, dtype=x.dtype, device="cuda"), torch.full((T + 5, H), 7.0, device="cuda")
