@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                         const float2 qf = NT == 1 ? qfreg : q_factor(nt);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float xv = fmaf(i & 1 ? qf.y : qf.x, acc[u][nt][i], -ref[nt][i & 1]);
+                            // rounded before ref comes off: scores past 2^24 would leave a product's lost bits otherwise
+                            float xv = __fmul_rn(i & 1 ? qf.y : qf.x, acc[u][nt][i]) - ref[nt][i & 1];
                             if (MASKED && !((see[u] >> (nt * 4 + i)) & 1)) xv = -INFINITY;
                             top = fmaxf(top, xv);
                             p[u][nt][i] = ex2(xv);
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                         for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                             for (int i = k; i < 4; i += 2) {
-                                const float sc = (k ? qf.y : qf.x) * acc[u][nt][i];
+                                const float sc = __fmul_rn(k ? qf.y : qf.x, acc[u][nt][i]);
                                 const float v = fmaxf(sc + lg[u][i >> 1], sc - 20.f);
                                 if (!MASKED || ((see[u] >> (nt * 4 + i)) & 1)) m = fmaxf(m, v);
                             }

@@ -10,7 +10,7 @@
 
 namespace qmm_impl {
 
-constexpr float kNoRef = -1e30f;  // reference of a query that has seen nothing yet
+constexpr float kNoRef = -3.402823466e38f;  // reference of a query that has seen nothing yet: below every score
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float ex2(float x) {

@@ -11,7 +11,8 @@
 //      columns of its own in tensor memory, and the biases into more.
 //   2. V: the row as RN_fp16(s q + b) (what qmm_dequantize gives).
 //   3. A softmax thread reads its position's sums: x = f * (bias + sum over groups of s * sum) - ref, all
-//      fp32, P = 2^x, and keeps its share of the rows' sums l in registers; P goes to shared memory as
+//      fp32 (the product rounded before ref comes off, so that the largest x is 0 however large the scores
+//      are), P = 2^x, and keeps its share of the rows' sums l in registers; P goes to shared memory as
 //      fp16 (for fp16 outputs as two terms, so that V's rounding is the only one before the output's).
 //   4. O^T += V^T P: V's rows as they are stored are the transposed (MN-major) operand, and so is P.
 //
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                         for (int j = 0; j < NG; ++j) tmem_ld(tmem_row + j * N + h0 + r0, sg[at][j]);
                     };
                     float p[HR];
-                    while (true) {
+                    for (bool moved = false;; moved = true) {
                         float top = -INFINITY;
                         read(0, 0);
 #pragma unroll
@@ -519,8 +520,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                                     uint64_t x = bits2(sb[at][i], sb[at][i + 1]);
 #pragma unroll
                                     for (int j = 0; j < NG; ++j) x = fma2(ks[j], bits2(sg[at][j][i], sg[at][j][i + 1]), x);
-                                    const float2 y = unpair(fma2(f[h], x, n[h]));
-                                    p[r0 + i] = y.x, p[r0 + i + 1] = y.y;
+                                    // rounded, as for the references, before those come off.  One by one: a packed
+                                    // product and a packed sum are made one operation by the assembler
+                                    const float2 y = unpair(mul2(f[h], x)), m = unpair(n[h]);
+                                    p[r0 + i] = __fadd_rn(y.x, m.x), p[r0 + i + 1] = __fadd_rn(y.y, m.y);
                                 }
                             }
                         }
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                         }
 #pragma unroll
                         for (int r = 0; r < HR; ++r) top = fmaxf(top, p[r]);
-                        if (!group_or(2, top > kMaxX)) break;
+                        if (moved || !group_or(2, top > kMaxX)) break;
                         // new references: the largest x of each row becomes 0.  x - ref has lost x where there was no
                         // reference yet, so the scores are taken from the sums again
                         if (any_tile) wait(bar_done, tile - 1);  // O is rescaled

@@ -158,6 +158,37 @@ def test_attention_scores_are_fp32(name):
     assert (lse.double() - want)[some].norm() <= 2.0 ** -21 * want[some].norm()
 
 
+@pytest.mark.parametrize("dtype,amp,scale", [(BF, 2.0 ** 20, 1.0), (BF, 2.0 ** 60, 0.125), (BF, -(2.0 ** 24), 1.0), (BF, -(2.0 ** 103), 0.25),
+                                             (HF, 60000.0, 1.0), (HF, 60000.0, 64.0), (HF, -60000.0, 8.0)])
+@pytest.mark.parametrize("heads,new", [(4, 1), (4, 3), (8, 6)])
+def test_attention_of_huge_scores(dtype, amp, scale, heads, new):
+    """Scores far past 2^24, where the next fp32 number is many powers of e away: each row is V at the position of
+    the largest score (others are 2^20 below it at least), and its lse that score.  Off by: V's or P * s's
+    rounding to fp16 (2^-11, by the value or by 8 scales), fp32 sums (2^-18 of the terms), the output's rounding;
+    the score by 2^-19 of its terms, all of one sign."""
+    n, dim, group = 300, 128, 64
+    c = filled_cache(8, 64, 2, dim, group, 31)
+    k = 50 + torch.rand((c.pages * 2 * 64, dim), device="cuda", generator=gen(5)) * 4
+    if amp > 0:
+        k -= 49
+    k = k.view(c.pages, 2, 64, dim)
+    table = ints([[3, 1, 0, 5, 7]])
+    best = 70  # of page 1
+    k[1, :, best - 64] += 49 if amp > 0 else -49
+    for a, part in zip(c.arrays()[:3], q.quantize(k.reshape(-1, dim).half(), 4, group)):
+        a.copy_(part.view(a.shape))
+    x = (amp * (0.5 + 0.5 * torch.rand((new, 2 * heads, dim), device="cuda", generator=gen(6)))).to(dtype)
+    o, lse = q.kv_attention(c, x, table, ints([n]), ints([0, new]), scale=scale)
+    (kc, ks, kb), (vc, vs, vb) = ref.rows_of(c.arrays(), table[0], [best], c.page_size)
+    want = (x.double().view(new, 2, heads, dim) * (ks * kc + kb)[None]).sum(-1).view(new, -1) * scale
+    assert ((lse.double() - want).abs() <= 2.0 ** -19 * want.abs()).all()
+    v, s = ((vs * vc + vb)[:, 0], vs[:, 0].amax(-1, keepdim=True))
+    bound = (2.0 ** -11 + 2.0 ** -14) * (8 * s + v.abs()) + 2.0 ** -18 * (16 * s + vb[:, 0].abs())
+    bound = bound + ref.SIXTEEN[dtype] * (v.abs() + bound)
+    err = (o.double().view(new, 2, heads, dim) - v[None, :, None]).abs()
+    assert (err <= bound[None, :, None]).all(), (err / bound[None, :, None]).max()
+
+
 def test_attention_strides_scale_and_outputs():
     """q as a slice of a fused projection's output at an odd offset, o and lse given, another scale."""
     c, x, table, lens, cu, _, _, _ = attention_case("ragged decodes")
