@@ -780,10 +780,12 @@ cudaError_t launch_attn(const AttnArgs& a, int head_dim, int group, cudaStream_t
     // taken to have half as many again (columns that a tile does not fill cost next to nothing)
     const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
     const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
-    // up to 32 rows (four columns) the warps' kernel is faster (8 sequences of 6 tokens of 4 heads over 16k
-    // positions: 53 us against 68), above them the tensor-core kernel, which takes 64 rows at a time (4 of 16
-    // tokens over 8k: 62 against 72); heads of 256 have two columns of the former only
-    if (rows > 32 && attn_tc_supported(head_dim)) return launch_attn_tc(a, head_dim, group, stream);
+    // The warps' kernel up to 32 rows of 128 (it streams the cache once up to there: 8 sequences of 6 tokens of 4
+    // heads over 16k positions take 56 us, the tensor-core kernel 71; 8 of 10 tokens over 4k 48 against 37), up to
+    // 512 of 64, whose two passes over the codes cost half (128 tokens of 4 heads over 8k positions: 56 us against
+    // 70; 16 sequences of 64 tokens over 2k in groups of 32: 85 against 82).  Heads of 256 have only the former
+    const int most_rows = head_dim == 64 ? 512 : 32;
+    if (rows > most_rows && attn_tc_supported(head_dim)) return launch_attn_tc(a, int(rows < 65536 ? rows : 65536), head_dim, group, stream);
     const int64_t cols = (rows + 7) / 8, most = head_dim == 256 ? 2 : 4;
     const AttnInst k = instance(head_dim, group, int(cols < most ? cols : most));
     return launch_attn_blocks(a, k.fn, k.threads, k.smem, k.slot, k.rows, kAttnUnit, k.blocks, 0, stream);

@@ -250,9 +250,9 @@ cudaError_t attn_blocks(void (*fn)(const AttnArgs), int smem, int per_sm, int re
 // Launches a kernel over the resident blocks, with its workspace.
 cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threads, int smem, int slot, int rows, int unit,
                                int per_sm, int regs, cudaStream_t stream);
-// The tensor-core kernel (qmm_attn_tc.cu).
+// The tensor-core kernel (qmm_attn_tc.cu).  query_rows: about how many a sequence and K/V head have.
 bool attn_tc_supported(int head_dim);
-cudaError_t launch_attn_tc(const AttnArgs& a, int head_dim, int group, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnArgs& a, int query_rows, int head_dim, int group, cudaStream_t stream);
 cudaError_t attn_tc_read_and_clear_errors(unsigned* out);
 
 }  // namespace qmm_impl

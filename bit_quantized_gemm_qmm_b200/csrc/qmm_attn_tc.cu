@@ -687,23 +687,25 @@ TcAttnInst inst() {
     using F = TcAttnFmt<D, GRP, N>;
     return TcAttnInst{attn_tc_kernel<D, GRP, N>, F::SMEM, F::SLOT, N};
 }
-// 64 rows at a time, where P goes in one term and the groups' columns leave room; else 32
+// Rows at a time: 32 take half as long to start and to finish, 64 convert the cache half as often.  64 where P
+// goes in one term, the groups' columns leave room, and a sequence has more than 256 rows (32 tokens of 4 heads
+// of 128 over 2k positions: 45 us with 64, 27 with 32; 64 tokens over 8k: 64 and 63; 256 tokens: 140 and 171).
 template <int D, int GRP>
-TcAttnInst inst_n(bool bf16) {
+TcAttnInst inst_n(bool wide) {
     if constexpr (D / GRP > 2) return inst<D, GRP, 32>();
-    else return bf16 ? inst<D, GRP, 64>() : inst<D, GRP, 32>();
+    else return wide ? inst<D, GRP, 64>() : inst<D, GRP, 32>();
 }
-TcAttnInst instance(int d, int grp, bool bf16) {
-    if (d == 64) return grp == 32 ? inst_n<64, 32>(bf16) : inst_n<64, 64>(bf16);
-    return grp == 32 ? inst_n<128, 32>(bf16) : grp == 64 ? inst_n<128, 64>(bf16) : inst_n<128, 128>(bf16);
+TcAttnInst instance(int d, int grp, bool wide) {
+    if (d == 64) return grp == 32 ? inst_n<64, 32>(wide) : inst_n<64, 64>(wide);
+    return grp == 32 ? inst_n<128, 32>(wide) : grp == 64 ? inst_n<128, 64>(wide) : inst_n<128, 128>(wide);
 }
 
 }  // namespace
 
 bool attn_tc_supported(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
-cudaError_t launch_attn_tc(const AttnArgs& a, int head_dim, int group, cudaStream_t stream) {
-    const TcAttnInst k = instance(head_dim, group, a.is_bf16 != 0);
+cudaError_t launch_attn_tc(const AttnArgs& a, int query_rows, int head_dim, int group, cudaStream_t stream) {
+    const TcAttnInst k = instance(head_dim, group, a.is_bf16 && query_rows > 256);
     return launch_attn_blocks(a, k.fn, kTcThreads, k.smem, k.slot, k.rows, kAttnTcUnit, 2, k.rows > 32 ? 128 : 0, stream);
 }
 

@@ -36,7 +36,7 @@ def many_rows(q, hk, seqs):
     """Whether the tensor-core kernel takes the call (launch_attn's rule)."""
     mean = -(-q.shape[0] // seqs)
     rows = (mean + mean // 2 if seqs > 1 else mean) * (q.shape[1] // hk)
-    return rows > 32 and q.shape[2] <= 128
+    return rows > {64: 512, 128: 32, 256: math.inf}[q.shape[2]]
 
 
 def attention(arrays, page, q, table, lens, cu, scale, window=0, tree=None):

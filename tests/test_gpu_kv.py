@@ -110,6 +110,10 @@ ATTENTION = {
     "many rows dim 64 group 32 fp16": (64, 32, 48, 2, 5, HF, [1000], [50], 0, False),
     "many rows dim 128 group 128 fp16": (128, 128, 16, 1, 12, HF, [500, 77], [12, 30], 0, False),
     "many rows dim 128 group 32": (128, 32, 64, 1, 8, BF, [640], [20], 0, False),
+    "prompt dim 64 group 64": (64, 64, 64, 1, 4, BF, [700], [200], 0, False),
+    "prompt dim 64 group 32": (64, 32, 16, 1, 6, BF, [300], [150], 0, False),
+    "prompt dim 64 fp16": (64, 32, 32, 1, 8, HF, [260, 131], [90, 40], 0, False),
+    "prompt dim 128 group 128": (128, 128, 32, 1, 4, BF, [500], [129], 0, False),
     "many rows long": (128, 64, 64, 1, 8, BF, [40000], [9], 0, False),
     "many rows, some empty": (128, 64, 64, 2, 4, BF, [0, 300, 10, 64], [20, 0, 30, 64], 0, False),
     "many rows window 200": (128, 64, 64, 2, 4, BF, [1500, 130], [100, 130], 200, False),
@@ -204,7 +208,7 @@ def test_attention_strides_scale_and_outputs():
     assert (out[:, 0] == 7).all() and (out[:, T + 1] == 7).all()
 
 
-@pytest.mark.parametrize("name", ["many rows dim 128 group 128", "many rows dim 64 group 32 fp16", "32 rows"])
+@pytest.mark.parametrize("name", ["many rows dim 128 group 128", "prompt dim 64 fp16", "32 rows"])
 def test_attention_strides_other_kernels(name):
     c, x, table, lens, cu, scale, _, _ = attention_case(name)
     T, H, D = x.shape
