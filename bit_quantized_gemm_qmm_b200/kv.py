@@ -283,16 +283,24 @@ class KVSequences:
         page = self.cache.page_size
         need = [-(-(self._lens[s] + n) // page) - len(self._pages[s]) for s, n in zip(seqs, new)]
         got = self._take(sum(need))
+        was = [(s, len(self._pages[s]), self._lens[s], self._drafts.get(s, 0)) for s in seqs]
         for s, n, m in zip(seqs, new, need):
             self._pages[s] += got[:m]
             del got[:m]
             self._lens[s] += n
             self._drafts[s] = n
-        flat, cols = self._table(seqs)
-        table, lens, cu = self._device(flat, [self._lens[s] for s in seqs], [sum(new[:i]) for i in range(len(new) + 1)])
-        table = table.reshape(len(seqs), cols)
-        kv_append(self.cache, k, v, table, lens, cu)
-        return kv_attention(self.cache, q, table, lens, cu, scale=scale, window=window, tree=tree)[0]
+        try:
+            flat, cols = self._table(seqs)
+            table, lens, cu = self._device(flat, [self._lens[s] for s in seqs], [sum(new[:i]) for i in range(len(new) + 1)])
+            table = table.reshape(len(seqs), cols)
+            kv_append(self.cache, k, v, table, lens, cu)
+            return kv_attention(self.cache, q, table, lens, cu, scale=scale, window=window, tree=tree)[0]
+        except Exception:  # a refused call leaves the sequences as they were
+            for s, pages, n, draft in was:
+                self._drop(self._pages[s][pages:])
+                del self._pages[s][pages:]
+                self._lens[s], self._drafts[s] = n, draft
+            raise
 
     def accept(self, seqs: list[int], keep: list[list[int]]) -> None:
         """Keeps some of the tokens of each sequence's last step (their numbers in it, rising) and

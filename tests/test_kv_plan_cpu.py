@@ -371,3 +371,24 @@ def test_bookkeeping_refusals(book):
     with pytest.raises(ValueError):
         s.accept([a], [])
     assert s.length(a) == 5
+
+
+@pytest.mark.parametrize("call", ["kv_append", "kv_attention"])
+def test_refused_step_changes_nothing(book, monkeypatch, call):
+    """A step whose calls refuse their arguments (a tree with a window, say) leaves lengths, pages and drafts."""
+    c, s = book
+    a, b = s.add(), s.add()
+    k = torch.zeros(9, 1, 64)
+    s.step([a, b], k, k, k, [6, 3])
+    pages = [s.pages(a), s.pages(b)]
+
+    def refuse(*args, **kwargs):
+        raise ValueError("refused")
+
+    with monkeypatch.context() as m:
+        m.setattr(kv, call, refuse)
+        with pytest.raises(ValueError, match="refused"):
+            s.step([b, a], k, k, k, [2, 7])
+    assert (s.length(a), s.length(b)) == (6, 3) and [s.pages(a), s.pages(b)] == pages and s.free_pages() == 37
+    s.accept([a, b], [[0, 5], [2]])
+    assert (s.length(a), s.length(b)) == (2, 1) and s.free_pages() == 38
