@@ -83,6 +83,16 @@ KvArgs kv_args(const qmm_kv_cache* c, const qmm_kv_seqs* s, const int32_t* at, i
     return a;
 }
 
+// Whether [tokens, heads] output rows of dim values do not overlap.  The rows of one index lie within the
+// other's step, so every layout that comes from slicing or transposing a dense tensor passes.
+bool rows_apart(int64_t tokens, int64_t heads, int64_t token_stride, int64_t head_stride, int64_t dim) {
+    const __int128 ts = token_stride < 0 ? -__int128(token_stride) : token_stride;
+    const __int128 hs = head_stride < 0 ? -__int128(head_stride) : head_stride;
+    if (tokens <= 1) return heads <= 1 || hs >= dim;
+    if (heads <= 1) return ts >= dim;
+    return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (tokens - 1) * ts + dim);
+}
+
 qmm_status check_dtype(qmm_dtype d) {
     return d == QMM_F16 || d == QMM_BF16 ? QMM_OK : fail(QMM_ERR_INVALID_ARG, "dtype=%d", int(d));
 }
@@ -120,6 +130,9 @@ qmm_status qmm_kv_gather(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, con
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16) ||
         (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 != 0)
         return fail(QMM_ERR_INVALID_ARG, "k and v must be 16-byte aligned, their strides multiples of 8 elements");
+    if (!rows_apart(tokens, cache->kv_heads, k_token_stride, k_head_stride, cache->head_dim) ||
+        !rows_apart(tokens, cache->kv_heads, v_token_stride, v_head_stride, cache->head_dim))
+        return fail(QMM_ERR_INVALID_ARG, "rows of k or v overlap");
     KvArgs a = kv_args(cache, seqs, starts, tokens);
     a.k_out = static_cast<uint16_t*>(k), a.v_out = static_cast<uint16_t*>(v);
     a.k_ts = k_token_stride, a.k_hs = k_head_stride, a.v_ts = v_token_stride, a.v_hs = v_head_stride;
@@ -169,6 +182,8 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const void* q, int64_t q_
     if (!q || !aligned(q, 2)) return fail(QMM_ERR_INVALID_ARG, "q must be a 2-byte aligned pointer");
     if (!o || !aligned(o, 8) || (o_token_stride | o_head_stride) % 4 != 0)
         return fail(QMM_ERR_INVALID_ARG, "o must be 8-byte aligned, its strides multiples of 4 elements");
+    if (!rows_apart(tokens, heads, o_token_stride, o_head_stride, cache->head_dim))
+        return fail(QMM_ERR_INVALID_ARG, "rows of o overlap");
     if (!aligned(lse, 4) || !aligned(tree, 8)) return fail(QMM_ERR_INVALID_ARG, "lse must be 4-byte and tree 8-byte aligned");
     AttnArgs a;
     std::memset(&a, 0, sizeof(a));

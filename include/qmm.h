@@ -329,8 +329,8 @@ qmm_status qmm_kv_append(const qmm_kv_cache* cache, const void* k, int64_t k_tok
 
 /*
  * qmm_kv_gather -- reads rows back as qmm_dequantize does: row cu_tokens[b] + i of k and v
- * ([tokens, kv_heads, head_dim], 16-byte aligned, strides multiples of 8 elements) becomes
- * position starts[b] + i of sequence b.
+ * ([tokens, kv_heads, head_dim], 16-byte aligned, strides multiples of 8 elements, rows that do
+ * not overlap) becomes position starts[b] + i of sequence b.
  */
 qmm_status qmm_kv_gather(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, const int32_t* starts,
                          int64_t tokens, void* k, int64_t k_token_stride, int64_t k_head_stride,
@@ -360,8 +360,8 @@ qmm_status qmm_kv_compact(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, co
  * qmm_kv_attention -- o = softmax(scale * q K^T + mask) V over the cache, for any number of new
  * tokens a sequence: one while decoding, a draft while verifying, a chunk of a prompt.
  *   q, o   [tokens, heads, head_dim] fp16/bf16 with the given strides (elements); q 2-byte, o
- *          8-byte aligned with strides multiples of 4.  Query head h reads K/V head
- *          h / (heads / kv_heads); heads up to 256, a multiple of kv_heads.
+ *          8-byte aligned with strides multiples of 4 and rows that do not overlap.  Query head h
+ *          reads K/V head h / (heads / kv_heads); heads up to 256, a multiple of kv_heads.
  *   lse    [tokens, heads] fp32, log sum exp(scale * q K^T + mask); may be null.
  *   lens   tokens of each sequence with the new ones, which are its last (as in qmm_kv_append,
  *          which comes first).  The token at position p sees positions <= p; with window > 0

@@ -212,6 +212,9 @@ def test_refuses_other_arguments(L):
     assert att(o=0) == 1 and att(o=12) == 1 and att(ostr=258) == 1 and att(lse=18) == 1 and att(tree=20) == 1
     gather = lambda k=16, stride=256: L.qmm_kv_gather(r(c), r(s), 16, 2, k, stride, 128, 16, 256, 128, 0, None)  # noqa: E731
     assert gather(k=24) == 1 and gather(stride=260) == 1
+    # output rows that overlap: broadcast tokens, tokens closer than their heads take
+    assert gather(stride=0) == 1 and gather(stride=128) == 1 and gather(stride=248) == 1 and gather(stride=-248) == 1
+    assert att(ostr=0) == 1 and att(ostr=252) == 1 and att(ostr=-252) == 1
     assert L.qmm_kv_copy_pages(r(c), 16, 16, -1, None) == 1 and L.qmm_kv_copy_pages(r(c), 16, 16, 2 ** 16 + 1, None) == 2
     assert L.qmm_kv_copy_pages(r(c), 0, 16, 1, None) == 1 and L.qmm_kv_copy_pages(r(c), 16, 18, 1, None) == 1
     assert L.qmm_kv_compact(r(c), r(s), 16, 0, 1, None) == 1 and L.qmm_kv_compact(r(c), r(s), 16, 18, 1, None) == 1
