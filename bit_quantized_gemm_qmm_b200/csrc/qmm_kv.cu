@@ -151,13 +151,15 @@ __device__ __forceinline__ Quantized quantize_words(const uint32_t (&raw)[4 * NW
     if (!bad && s != 0.f) {
         // rint(RN(d / s)) from t = d * RN(1 / s), which is within 2^-22 of d / s in relative terms: it has the
         // same nearest whole number unless it lies within 2^-12 of a half.  No code leaves [0, 15] where the
-        // bias is off by less than 0.4 s (fp16's half step, 2^-11 of it or 2^-25), as the scale's own rounding
-        // moves the last code by 15 * 2^-11.  Elsewhere the divisions themselves decide.
+        // bias is off by less than 0.4 s (fp16's half step, 2^-11 of it or 2^-25) and the scale is a normal fp16
+        // number, whose own rounding moves the last code by 15 * 2^-11 at most (a subnormal one is off by up to
+        // 2^-25 whatever its size: at 2 * 2^-24 the last code may be 18).  Elsewhere the divisions themselves
+        // decide, and their codes are clamped.
         const float inv = __frcp_rn(s);
         constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
         const uint64_t nb = pack2(-bf, -bf), inv2 = pack2(inv, inv), whole = pack2(kWhole, kWhole), nwhole = pack2(-kWhole, -kWhole);
         const uint64_t ninv2 = pack2(-inv, -inv);
-        float off = fmaxf(fabsf(bf) * 0x1p-11f, 0x1p-25f) > 0.4f * s ? 1.f : 0.f;
+        float off = s < 0x1p-14f || fabsf(bf) * 0x1p-11f > 0.4f * s ? 1.f : 0.f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
             uint32_t word = 0;
