@@ -23,9 +23,10 @@
 // movmatrix turns the packed P * s round.
 //
 // Softmax: each warp keeps a reference per query, not the maximum: x - ref goes through ex2 and
-// the sums are rescaled only when some P * s reaches 2 (one OR over the packed values: the sign
-// of a large or NaN fp16 is bit 14) or x - ref reaches 60.  The reference is then put so that
-// the largest P * s of the tile is 2^-4.
+// the sums are rescaled only when some P * s reaches 2^15 or x - ref reaches 60.  The reference is then
+// put so that the largest P * s of the tile is 2^10: fp16 rounds by 2^-11 down to 2^-24 of that, whatever the
+// weight of a position and however small a group's V beside the others' (with the largest at 2^-4 all that
+// lay 2^-20 below it was lost; the wider range costs 1 us of 69 where 32 sequences of up to 16,384 decode).
 //
 // Work: units of 32 positions of one (sequence, K/V head, row tile) are dealt out evenly over
 // the resident blocks (qmm_kv_plan.h), whatever the lengths; a block's warps take them in turn, each
@@ -63,6 +64,17 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
 __device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Of three, in one instruction: the largest, and the largest magnitude (NaN are passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
@@ -471,21 +483,23 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
             float p[SUBS][COLS][4];
             uint32_t pk[SUBS][COLS][NG][2];
             auto probabilities = [&]() -> bool {
-                uint32_t any = 0;
+                float most = 0.f;
                 float top = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                     for (int nt = 0; nt < COLS; ++nt) {
                         const float2 qf = NT == 1 ? qfreg : q_factor(nt);
+                        float xs[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             // rounded before ref comes off: scores past 2^24 would leave a product's lost bits otherwise
                             float xv = __fmul_rn(i & 1 ? qf.y : qf.x, acc[u][nt][i]) - ref[nt][i & 1];
                             if (MASKED && !((see[u] >> (nt * 4 + i)) & 1)) xv = -INFINITY;
-                            top = fmaxf(top, xv);
+                            xs[i] = xv;
                             p[u][nt][i] = ex2(xv);
                         }
+                        top = max3(max3(top, xs[0], xs[1]), xs[2], xs[3]);
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
                             float m[4];
@@ -496,13 +510,15 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                             }
                             pk[u][nt][j][0] = f32x2_to_f16x2(m[0], m[1]);
                             pk[u][nt][j][1] = f32x2_to_f16x2(m[2], m[3]);
-                            any |= pk[u][nt][j][0] | pk[u][nt][j][1];
+                            most = max3_abs(max3_abs(most, m[0], m[1]), m[2], m[3]);
                         }
                     }
-                return (any & 0x40004000u) != 0 || top > 60.f;
+                return fabsf(most) >= 32768.f || top > 60.f;  // 2^15 is 0x7800
             };
             if (__any_sync(kFull, probabilities())) {
-                // new references from these positions: the largest P * s becomes 2^-4 (and P at most 2^20)
+                // New references from these positions: the largest P * s becomes 2^10, or P is 1 where s alone is
+                // larger (and at most 2^34: s is 2^-24 at least, or nothing).  The reference is rounded towards
+                // the score, so that scores far past 2^24 leave P between 1 and what it should be
                 float lg[SUBS][2];
 #pragma unroll
                 for (int u = 0; u < SUBS; ++u)
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                         float m = 0.f;
 #pragma unroll
                         for (int j = 0; j < NG; ++j) m = fmaxf(m, fabsf(vs[u][k][j]));
-                        lg[u][k] = lg2(m) + 4.f;
+                        lg[u][k] = fminf(fmaxf(lg2(m) - 10.f, -34.f), 0.f);
                     }
 #pragma unroll
                 for (int nt = 0; nt < COLS; ++nt) {
@@ -524,7 +540,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
 #pragma unroll
                             for (int i = k; i < 4; i += 2) {
                                 const float sc = __fmul_rn(k ? qf.y : qf.x, acc[u][nt][i]);
-                                const float v = fmaxf(sc + lg[u][i >> 1], sc - 20.f);
+                                const float v = __fadd_ru(sc, lg[u][i >> 1]);
                                 if (!MASKED || ((see[u] >> (nt * 4 + i)) & 1)) m = fmaxf(m, v);
                             }
 #pragma unroll

@@ -31,6 +31,14 @@ __device__ __forceinline__ float half_hi(uint32_t v) { return __half2float(__ush
 // normal numbers (without it the second would be subnormal, and the sum good to 2^-18 only).
 constexpr float kSumUp = 131072.f;
 
+// Natural log of l * 2^ref.  l may be far from one: its power of two is added exactly.
+__device__ __forceinline__ float lse_of(float ref, float l) {
+    if (l == 0.f) return -INFINITY;
+    if (!(l < INFINITY)) return l;
+    const uint32_t u = __float_as_uint(l);
+    return (ref + float(int(u >> 23) - 127) + lg2(__uint_as_float((u & 0x7FFFFFu) | 0x3F800000u))) * 0.693147180559945309f;
+}
+
 // Four values of an output row: sum / l, rounded once; with the first of them the row's lse.
 // A row that saw nothing (l = 0) is zeros and -infinity.
 __device__ __forceinline__ void store_row4(const AttnArgs& a, int row, int head, int d, float4 v, float l, float ref) {
@@ -45,8 +53,7 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int row, int head,
     }
     *reinterpret_cast<uint2*>(a.o + int64_t(row) * a.o_ts + int64_t(head) * a.o_hs + d) = out;
     if (d == 0 && a.lse != nullptr)
-        a.lse[int64_t(row) * (a.kv_heads * a.group_heads) + head] =
-            l == 0.f ? -INFINITY : (ref + lg2(l)) * 0.693147180559945309f;
+        a.lse[int64_t(row) * (a.kv_heads * a.group_heads) + head] = lse_of(ref, l);
 }
 
 // How a kernel cuts the work: query rows a tile, positions a unit, warps that take units of their own, and what

@@ -47,3 +47,80 @@ def test_append_of_tiny_groups(dtype, group, tokens):
             wrong = (got != want).any(-1)
             assert not wrong.any(), f"{int(wrong.sum())} of {wrong.numel()} rows differ from quantize()'s"
     assert q.device_errors() == 0
+
+
+# dim, group, heads a kv head, new tokens: the warps' kernel with one to four columns of query rows, the tensor-core kernel
+@pytest.mark.parametrize("dim,group,grp,new", [(128, 64, 4, 2), (128, 32, 8, 1), (128, 64, 4, 4), (128, 64, 4, 5), (128, 32, 4, 8),
+                                               (64, 32, 4, 2), (256, 64, 4, 2), (256, 32, 4, 3), (128, 64, 4, 12)])
+@pytest.mark.parametrize("ratio", [8, 14])
+def test_attention_of_v_groups_of_different_scale(dim, group, grp, new, ratio):
+    """V's first group 2^ratio times the others: those are as exact as if they stood alone.
+
+    Off, for a value of a group: the scores' and the sums' share, 2^-11 of each P * s times |code - 8| (the
+    tensor-core kernel: of each P |v|), the output's rounding; and where a P * s lies 2^24 below the row's
+    largest over all groups, so that it is subnormal in fp16, 2^-35 of that largest one, times 8."""
+    n, hk, page = 1500, 2, 64
+    table, pages = one_sequence(n, page)
+    c = q.KVCache.empty(pages, page, hk, dim, group)
+    k = torch.randn((n, hk, dim), device="cuda", generator=gen(3)).half()
+    v = torch.randn((n, hk, dim), device="cuda", generator=gen(4)) * 4
+    v[..., group:] *= 2.0 ** -ratio
+    x = torch.randn((new, hk * grp, dim), device="cuda", generator=gen(5)).half()
+    cu = ints([0, new])
+    q.kv_append(c, k, v.half(), table, ints([n]), ints([0, n]))
+    o, lse = q.kv_attention(c, x, table, ints([n]), cu)
+    want, wl, _, bl = ref.attention(c.arrays(), page, x, table, [n], [0, new], dim ** -0.5)
+    assert ((lse.double() - wl).abs() <= bl).all()
+    (kc, ks, kb), (vc, vs, vb) = ref.rows_of(c.arrays(), table[0], range(n), page)
+    many = ref.many_rows(x, hk, 1)
+    for i in range(new):
+        m = n - new + i + 1
+        for h in range(hk):
+            hs = slice(h * grp, (h + 1) * grp)
+            xq = x[i, hs].double()
+            w = torch.softmax(xq @ (ks * kc + kb)[h, :m].T * dim ** -0.5, -1)
+            size = xq.abs() @ (ks * kc + kb.abs())[h, :m].T * dim ** -0.5
+            dx = 2.0 ** -19 * size.amax(-1, keepdim=True)
+            s, code, b = vs[h, :m], vc[h, :m], vb[h, :m].abs()
+            bound = (2 * dx + 2.0 ** -19) * (w @ (s * code + b + 8 * s))
+            if many:
+                bound = bound + 2.0 ** -11 * (w @ (s * code + vb[h, :m]).abs()) + 2.0 ** -25
+            else:
+                ps = w[..., None] * s
+                top = ps.amax((1, 2), keepdim=True)
+                bound = bound + 2.0 ** -11 * (w @ (s * (code - 8).abs())) + ((ps < top * 2.0 ** -24).sum(1) * 2.0 ** -32) * top[:, 0]
+            bound = bound + 2.0 ** -11 * (want[i, hs].abs() + bound) + 2.0 ** -25
+            err = (o[i, hs].double() - want[i, hs]).abs()
+            assert (err <= bound).all(), f"{(err / bound).max():.3g} of the bound, {(err / bound)[:, group:].max():.3g} past the first group"
+
+
+@pytest.mark.parametrize("seqs,grp", [(1, 1), (600, 1), (1, 4)])
+def test_attention_beside_one_large_weight(seqs, grp):
+    """A first position whose weight is 2^21.2 times that of each of the 99,999 others (they hold 4%
+    together), read by many blocks and by one: the others count with what they hold.
+
+    Off: the fp16 roundings of P * s (2^-11, times |code - 8|) or of V (2^-11 |v|), sums of fp32 that the matrix
+    units truncate (2^-23 of the sum each step; a warp takes every fourth unit of 32 positions, two steps a unit;
+    the tensor-core kernel every step of 16 itself), the scores' share (2^-19 of their size), the output's rounding."""
+    n, dim, group, page = 100000, 128, 64, 1024
+    table, pages = one_sequence(n, page)
+    c = q.KVCache.empty(pages, page, 1, dim, group)
+    for a, j in ((c.k_packed, 1), (c.v_packed, 2)):
+        a.copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, a.shape, device="cuda", generator=gen(j)))
+    c.v_packed.bitwise_or_(-0x33333334)  # codes 12 to 15
+    c.v_scales.fill_(0.1), c.v_biases.fill_(0.5)  # K is zero, but for
+    x = torch.ones((seqs, grp, dim), device="cuda", dtype=HF)
+    many = ref.many_rows(x, 1, seqs)
+    c.k_biases[int(table[0, 0]), 0, 0] = (23.42 if many else 21.2) * math.log(2) / dim ** 0.5
+    o, lse = q.kv_attention(c, x, table.expand(seqs, pages).contiguous(), ints([n] * seqs), ints(list(range(seqs + 1))))
+    (kc, ks, kb), (vc, vs, vb) = ref.rows_of(c.arrays(), table[0], range(n), page)
+    score = (ks * kc + kb)[0].sum(-1) * dim ** -0.5
+    w = torch.softmax(score, -1)
+    want, terms = w @ (vs * vc + vb)[0], w @ (vs * (vc + 8) + vb)[0]
+    # a thread adds every 64th position or pair of positions (every 128th) to its sum, rounded by 2^-24 each time
+    assert ((lse.double() - torch.logsumexp(score, -1)).abs() <= 2.0 ** -19 * score[0] + 2.0 ** -20 + n / 64 * 2.0 ** -24).all()
+    steps = n / 16 if many else n / 64
+    bound = 2.0 ** -11 * (want.abs() if many else w @ (vs * (vc - 8).abs())[0]) + (steps * 2.0 ** -23 + 2.0 ** -18 * score[0]) * terms
+    bound = bound + 2.0 ** -11 * (want + bound)
+    err = (o.double() - want).abs()
+    assert (err <= bound).all(), f"off by {err.max():.3g}, {(err / bound).max():.3g} of the bound"
