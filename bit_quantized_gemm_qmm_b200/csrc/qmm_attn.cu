@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                     for (int k = 0; k < 2; ++k) {
                         float m = 0.f;
 #pragma unroll
-                        for (int j = 0; j < NG; ++j) m = fmaxf(m, fabsf(vs[u][k][j]));
+                        for (int j = 0; j < NG; ++j) m = fmaxf(m, fabsf(vs[u][k][j]) < INFINITY ? fabsf(vs[u][k][j]) : 0.f);
                         lg[u][k] = fminf(fmaxf(lg2(m) - 10.f, -34.f), 0.f);
                     }
 #pragma unroll

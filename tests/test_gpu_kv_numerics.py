@@ -7,7 +7,7 @@ import torch
 
 import bit_quantized_gemm_qmm_b200 as q
 import kv_reference as ref
-from test_gpu_kv import BF, HF, gen, ints
+from test_gpu_kv import BF, HF, filled_cache, gen, ints, page_tables
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,37 @@ def test_attention_beside_one_large_weight(seqs, grp):
     bound = bound + 2.0 ** -11 * (want + bound)
     err = (o.double() - want).abs()
     assert (err <= bound).all(), f"off by {err.max():.3g}, {(err / bound).max():.3g} of the bound"
+
+
+def poke(c, table, pos, group, **constants):
+    """Sets a position's constants of one group of V (of all heads); its codes become 15."""
+    pg, r = int(table[pos // c.page_size]), pos % c.page_size
+    c.v_packed[pg, :, r] = -1
+    for name, value in constants.items():
+        getattr(c, name)[pg, :, r, group] = value
+
+
+@pytest.mark.parametrize("dim,group,grp,new", [(128, 64, 4, 2), (128, 32, 4, 6), (64, 64, 4, 2), (256, 64, 4, 3)])
+@pytest.mark.parametrize("name,value", [("v_scales", math.inf), ("v_scales", math.nan), ("v_biases", -math.inf), ("v_biases", math.nan)])
+@pytest.mark.parametrize("at", [3, 697])
+def test_attention_of_v_that_is_not_finite(dim, group, grp, new, name, value, at):
+    """A position of the last group of V that holds an infinity or NaN: the lse knows nothing of it, nor do
+    the other groups, nor the rows that do not see it."""
+    n, hk, page = 700, 2, 64
+    c = filled_cache(12, page, hk, dim, group, 1)
+    table = page_tables([n], page, 12, 2)
+    x = torch.randn((new, hk * grp, dim), device="cuda", generator=gen(5)).to(BF)
+    lens, cu = ints([n]), ints([0, new])
+    want, wl, bo, bl = ref.attention(c.arrays(), page, x, table, [n], [0, new], dim ** -0.5)
+    poke(c, table[0], at, -1, **{name: value})
+    if group < dim:  # its codes are others now
+        keep = ref.attention(c.arrays(), page, x, table, [n], [0, new], dim ** -0.5)
+        want[..., :-group], bo[..., :-group] = keep[0][..., :-group], keep[2][..., :-group]
+    o, lse = q.kv_attention(c, x, table, lens, cu)
+    assert ((lse.double() - wl).abs() <= bl).all()
+    sees = torch.arange(new, device="cuda") + n - new >= at
+    assert not o[sees][..., -group:].isfinite().any()
+    ok = torch.ones_like(o, dtype=torch.bool)
+    ok[sees, :, -group:] = False
+    err = (o.double() - want).abs()
+    assert (err[ok] <= bo[ok]).all(), f"off by {err[ok].max():.3g}"
