@@ -66,7 +66,8 @@ struct TcAttnFmt {
     static constexpr int OFF_POS = OFF_RED + 4 * N * 4;    // per position, for two tiles: K's scales, what is the matter
     static constexpr int OFF_BAR = OFF_POS + 2 * kPos * (NG + 1) * 4;
     static constexpr int OFF_RUN = OFF_BAR + 64;       // this run and the next
-    static constexpr int USED = OFF_RUN + 2 * 96;
+    static constexpr int OFF_NAN = OFF_RUN + 2 * 96;   // per group, bit per row: it sees a V that is not finite
+    static constexpr int USED = OFF_NAN + NG * 8;
     static constexpr int SMEM = (USED > 80 * 1024 ? USED : 80 * 1024) + 1024;  // two blocks an SM at most; alignment
     // tensor memory columns: group sums, biases, O^T
     static constexpr int COL_B = NG * N, COL_O = COL_B + N;
@@ -146,7 +147,7 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// What is the matter with a position (OFF_POS): it is not there; its V is not finite.
+// What is the matter with a position (OFF_POS): it is not there; its V is zeroed, because not finite, in group j (kOdd << j).
 constexpr uint32_t kAbsent = 1, kOdd = 2;
 
 template <int D, int GRP, int N>
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
 
     // ---- Q of the current run: K-major panels, scaled by a power of two per row (as in qmm_attn.cu)
     auto stage_q = [&]() {
+        if (tid < 2 * NG) reinterpret_cast<uint32_t*>(smem + F::OFF_NAN)[tid] = 0;
         auto load = [&](int i) {
             const int qr = cur->row_lo + i / WORDS, tok = qr / a.group_heads, hg = qr - tok * a.group_heads;
             if (i / WORDS >= cur->rows) return make_uint4(0u, 0u, 0u, 0u);
@@ -355,14 +357,20 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 const bool there = row >= 0;
                 const bool masked = !(cur->t0 + kPos * u >= cur->full_lo && cur->t0 + kPos * (u + 1) <= cur->full_hi);
                 const int u_next = seek(cur, u + 1);
+                // V's constants: rows that are not there are zeros.  Where a tile is masked, a group that is not finite
+                // is zeros too; the softmax notes which query rows see it, and those become NaN at the end
+                uint32_t vsb[NG], state = there ? 0u : kAbsent;
                 bool odd = false;
 #pragma unroll
-                for (int j = 0; j < NG; ++j) odd |= (vsr[j] & 0x7C00) == 0x7C00 || (vbr[j] & 0x7C00) == 0x7C00;
-                // V's constants: rows that are not there are zeros.  Where a tile is masked, a row that is not finite
-                // is zeros too, and rows that see it become NaN through their score
-                uint32_t vsb[NG];
+                for (int j = 0; j < NG; ++j) {
+                    vsb[j] = there ? uint32_t(vsr[j]) | uint32_t(vbr[j]) << 16 : 0u;
+                    odd |= (((vsb[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;  // an exponent of ones
+                }
+                if (masked && odd) {
 #pragma unroll
-                for (int j = 0; j < NG; ++j) vsb[j] = !there || (masked && odd) ? 0u : uint32_t(vsr[j]) | uint32_t(vbr[j]) << 16;
+                    for (int j = 0; j < NG; ++j)
+                        if ((((vsb[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0) vsb[j] = 0, state |= kOdd << j;
+                }
                 // ---- K, and the scores' MMAs
                 if (tile) wait(bar_full, tile - 1);
 #pragma unroll
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                     if (3 * NG > 8) sts_v4(sbase + F::OFF_KB + kPos * 16 + me * 16, make_uint4(c[4], c[5], c[6], c[7]));
                 }
                 uint32_t* const pos = reinterpret_cast<uint32_t*>(smem + F::OFF_POS) + (tile & 1) * kPos * (NG + 1) + me;
-                pos[NG * kPos] = (there ? 0u : kAbsent) | (odd ? kOdd : 0u);
+                pos[NG * kPos] = state;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) pos[j * kPos] = __float_as_uint(__half2float(__ushort_as_half(ksr[j])) * kSumUp);
                 fence_async_smem();
@@ -493,9 +501,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                                 }
                                 see |= on << r;
                             }
+#pragma unroll 1
+                            for (int j = 0; j < NG && state >= kOdd << j; ++j)
+                                if (state & (kOdd << j)) atomicOr(reinterpret_cast<uint32_t*>(smem + F::OFF_NAN) + 2 * j + h0 / 32, see);
                         }
                     }
-                    const bool all = see == 0xFFFFFFFFu && !(masked && (state & kOdd));
+                    const bool all = see == 0xFFFFFFFFu;
                     // the sums of rows [r0, r0 + CH) of this half, as a ring of two: one is read while the other is used
                     uint32_t sb[2][CH], sg[2][NG][CH];
                     auto read = [&](int at, int r0) {
@@ -530,9 +541,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                             }
                         }
                         if (!all) {
-                            const bool odd = masked && (state & kOdd);
 #pragma unroll
-                            for (int r = 0; r < HR; ++r) p[r] = (see >> r) & 1 ? (odd ? NAN : p[r]) : -INFINITY;
+                            for (int r = 0; r < HR; ++r) p[r] = (see >> r) & 1 ? p[r] : -INFINITY;
                         }
 #pragma unroll
                         for (int r = 0; r < HR; ++r) top = fmaxf(top, p[r]);
@@ -642,12 +652,19 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
             group_sync(2);
             // this thread's d: the codes' order within a word
             const int o8 = me & 7, d = (me & ~7) + (o8 >> 1) + (o8 & 1) * 4;
+            const uint32_t* const nan = reinterpret_cast<const uint32_t*>(smem + F::OFF_NAN) + (me < D ? me / GRP * 2 : 0);
+            const bool some = (nan[0] | nan[1]) != 0;
 #pragma unroll 1
             for (int r0 = 0; r0 < N; r0 += CH) {
                 if (r0 >= cur->rows) break;
                 uint32_t o[CH];
                 tmem_ld(tmem_row + F::COL_O + r0, o);
                 tc_wait_ld();
+                if (some) {
+                    const uint32_t odd = nan[r0 >> 5] >> (r0 & 31);
+#pragma unroll
+                    for (int k = 0; k < CH; ++k) o[k] = (odd >> k) & 1 ? 0x7FFFFFFFu : o[k];
+                }
 #pragma unroll
                 for (int k = 0; k < CH; ++k) {
                     const int r = r0 + k;

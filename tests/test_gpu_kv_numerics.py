@@ -134,7 +134,8 @@ def poke(c, table, pos, group, **constants):
         getattr(c, name)[pg, :, r, group] = value
 
 
-@pytest.mark.parametrize("dim,group,grp,new", [(128, 64, 4, 2), (128, 32, 4, 6), (64, 64, 4, 2), (256, 64, 4, 3)])
+@pytest.mark.parametrize("dim,group,grp,new", [(128, 64, 4, 2), (128, 32, 4, 6), (64, 64, 4, 2), (256, 64, 4, 3), (128, 64, 4, 20),
+                                             (128, 64, 4, 100), (128, 32, 4, 33), (64, 32, 16, 60), (128, 128, 8, 50)])
 @pytest.mark.parametrize("name,value", [("v_scales", math.inf), ("v_scales", math.nan), ("v_biases", -math.inf), ("v_biases", math.nan)])
 @pytest.mark.parametrize("at", [3, 697])
 def test_attention_of_v_that_is_not_finite(dim, group, grp, new, name, value, at):
