@@ -9,7 +9,8 @@
 //      subnormal q * 2^-24, one place up q * 2^-20; the factor 16 is in Q), and its biases as 16 more
 //      columns against three fp16 terms of each group's sum of Q.  tcgen05.mma sums each group into
 //      columns of its own in tensor memory, and the biases into more.
-//   2. V: the row as RN_fp16(s q + b) (what qmm_dequantize gives).
+//   2. V: the row as RN_fp16(s q + b) (what qmm_dequantize gives); where that passes fp16's range, 2^-5 times it,
+//      and the position's P 2^5 times.
 //   3. A softmax thread reads its position's sums: x = f * (bias + sum over groups of s * sum) - ref, all
 //      fp32 (the product rounded before ref comes off, so that the largest x is 0 however large the scores
 //      are), P = 2^x, and keeps its share of the rows' sums l in registers; P goes to shared memory as
@@ -147,8 +148,10 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// What is the matter with a position (OFF_POS): it is not there; its V is zeroed, because not finite, in group j (kOdd << j).
-constexpr uint32_t kAbsent = 1, kOdd = 2;
+// What is the matter with a position (OFF_POS): it is not there; its V is past fp16, and kept 2^-5 times what it
+// is; its V is zeroed, because not finite, in group j (kOdd << j).
+constexpr uint32_t kAbsent = 1, kFar = 2, kOdd = 4;
+constexpr int kFarShift = 5;  // 15 |s| + |b| is below 2^20
 
 template <int D, int GRP, int N>
 __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
@@ -364,12 +367,21 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     vsb[j] = there ? uint32_t(vsr[j]) | uint32_t(vbr[j]) << 16 : 0u;
-                    odd |= (((vsb[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;  // an exponent of ones
+                    // 15 s + b, the value furthest from b, is infinite or NaN (so it is if s or b are)
+                    odd |= (hfma2(vsb[j], 0x4B804B80u, vsb[j] >> 16) & 0x7C00u) == 0x7C00u;
                 }
-                if (masked && odd) {
+                if (odd) {
+                    // Finite constants whose values pass fp16's range: V counts 2^-5 times, its probability 2^5 times (its
+                    // other groups may lose what lies below 2^-16)
 #pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        if ((((vsb[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0) vsb[j] = 0, state |= kOdd << j;
+                    for (int j = 0; j < NG; ++j) {
+                        const bool inf = (((vsb[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;  // an exponent of ones
+                        if (!inf && (hfma2(vsb[j], 0x4B804B80u, vsb[j] >> 16) & 0x7C00u) == 0x7C00u) state |= kFar;
+                        if (masked && inf) vsb[j] = 0, state |= kOdd << j;
+                    }
+                    if (state & kFar)
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) vsb[j] = hfma2(vsb[j], 0x28002800u, 0x80008000u);  // 2^-5; -0 added
                 }
                 // ---- K, and the scores' MMAs
                 if (tile) wait(bar_full, tile - 1);
@@ -506,7 +518,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                                 if (state & (kOdd << j)) atomicOr(reinterpret_cast<uint32_t*>(smem + F::OFF_NAN) + 2 * j + h0 / 32, see);
                         }
                     }
-                    const bool all = see == 0xFFFFFFFFu;
+                    const bool all = see == 0xFFFFFFFFu && !(state & kFar);
+                    const float up = state & kFar ? float(kFarShift) : 0.f;
                     // the sums of rows [r0, r0 + CH) of this half, as a ring of two: one is read while the other is used
                     uint32_t sb[2][CH], sg[2][NG][CH];
                     auto read = [&](int at, int r0) {
@@ -542,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                         }
                         if (!all) {
 #pragma unroll
-                            for (int r = 0; r < HR; ++r) p[r] = (see >> r) & 1 ? p[r] : -INFINITY;
+                            for (int r = 0; r < HR; ++r) p[r] = (see >> r) & 1 ? p[r] + up : -INFINITY;
                         }
 #pragma unroll
                         for (int r = 0; r < HR; ++r) top = fmaxf(top, p[r]);
@@ -560,7 +573,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                                 float x = __uint_as_float(sb[0][k]);
 #pragma unroll
                                 for (int j = 0; j < NG; ++j) x = fmaf(unpair(ks[j]).x, __uint_as_float(sg[0][j][k]), x);
-                                x *= reinterpret_cast<const float*>(smem + F::OFF_F)[h0 + r0 + k];
+                                x = __fadd_rn(__fmul_rn(x, reinterpret_cast<const float*>(smem + F::OFF_F)[h0 + r0 + k]), up);
                                 const float m = warp_max((see >> (r0 + k)) & 1 ? x : -INFINITY);
                                 if (lane == 0) red[w * N + h0 + r0 + k] = m;
                             }
@@ -598,6 +611,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                         tc_fence_before();
                         mbar_arrive(bar_free);
                     }
+                    // (l's share of a P kept 2^5 times what it is)
+                    const float lw = state & kFar ? 1.f / (1 << kFarShift) : 1.f;
                     if (any_tile && h0 == 0) wait(bar_done, tile - 1);  // P's place is free
 #pragma unroll
                     for (int r0 = 0; r0 < HR; r0 += 8) {
@@ -605,7 +620,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float p0 = ex2(p[r0 + 2 * k]), p1 = ex2(p[r0 + 2 * k + 1]);
-                            l[(h0 + r0) / 2 + k] = add2(l[(h0 + r0) / 2 + k], pair(p0, p1));
+                            l[(h0 + r0) / 2 + k] = fma2(pair(p0, p1), pair(lw, lw), l[(h0 + r0) / 2 + k]);
                             h[k] = f32x2_to_f16x2(p0, p1);
                             p[r0 + 2 * k] = p0, p[r0 + 2 * k + 1] = p1;
                         }

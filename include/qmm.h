@@ -374,9 +374,10 @@ qmm_status qmm_kv_compact(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, co
  * its row's largest value (exact unless 2^-24 below it); scores, softmax and sums are fp32; o is
  * rounded once.  Up to 32 query rows a K/V head (new tokens times query heads; 512 at head_dim 64,
  * any number at 256) V's codes are exact too and each probability times V's scale is rounded once to
- * fp16 (by 2^-11, or below 2^-24 of the row's largest such product over all groups by 2^-35 of that); above, V is rounded to fp16 as qmm_dequantize does (|V| beyond 65504 there becomes infinity),
- * and probabilities are fp16 for bf16 outputs and two fp16 terms for fp16 outputs.  Which of the
- * two runs goes by tokens / seqs, not by the lengths.  Results do not depend on timing.
+ * fp16 (by 2^-11, or below 2^-24 of the row's largest such product over all groups by 2^-35 of that);
+ * above, V is rounded to the 11 bits of fp16, past its range too, and probabilities are fp16 for bf16
+ * outputs and two fp16 terms for fp16 outputs.  Which of the two runs goes by tokens / seqs, not by the
+ * lengths.  Results do not depend on timing.
  * Uses the stream's workspace (as qmm), a captured call one of its capture: two instances of one
  * captured graph must not run at once.  The tiles of 8 query rows or more that the new tokens make,
  * times kv_heads, times max_pages * page_size / 32, must stay below 2^29.

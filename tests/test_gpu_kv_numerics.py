@@ -7,7 +7,7 @@ import torch
 
 import bit_quantized_gemm_qmm_b200 as q
 import kv_reference as ref
-from test_gpu_kv import BF, HF, filled_cache, gen, ints, page_tables
+from test_gpu_kv import BF, HF, check, filled_cache, gen, ints, page_tables
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,33 @@ def test_attention_of_v_that_is_not_finite(dim, group, grp, new, name, value, at
     ok[sees, :, -group:] = False
     err = (o.double() - want).abs()
     assert (err[ok] <= bo[ok]).all(), f"off by {err[ok].max():.3g}"
+
+
+@pytest.mark.parametrize("dim,group,grp,new,dtype", [(128, 64, 4, 20, HF), (128, 64, 4, 20, BF), (128, 64, 4, 100, BF), (128, 32, 4, 20, HF),
+                                                     (128, 128, 8, 9, BF), (64, 32, 16, 60, HF), (64, 64, 16, 60, BF), (128, 64, 4, 2, HF)])
+@pytest.mark.parametrize("mask", ["causal", "tree", "window", "seen by all"])
+def test_attention_of_v_beyond_fp16(dim, group, grp, new, dtype, mask):
+    """V whose finite constants give values past 65504 (60000 + 15 * 400): nothing to the rows that do not see it,
+    itself to those that do."""
+    n, hk, page = 700, 2, 64
+    c = filled_cache(12, page, hk, dim, group, 1)
+    table = page_tables([n], page, 12, 2)
+    x = torch.randn((new, hk * grp, dim), device="cuda", generator=gen(5)).to(dtype)
+    window, tree = 0, None
+    if mask == "causal":
+        at = [n - 1, n - new // 2]
+    elif mask == "tree":
+        at = [n - new + 1]
+        tree = torch.randint(-2 ** 62, 2 ** 62, (new,), device="cuda", generator=gen(6)) | 1
+    elif mask == "window":
+        at, window = [n - 100 - new // 2, 100], 100
+    else:
+        at = [5, 300]
+    for p in at:
+        poke(c, table[0], p, -1, v_scales=400.0, v_biases=60000.0)
+    lens, cu = ints([n]), ints([0, new])
+    o, lse = q.kv_attention(c, x, table, lens, cu, window=window, tree=tree)
+    want = ref.attention(c.arrays(), page, x, table, [n], [0, new], dim ** -0.5, window, tree)
+    assert want[0].abs().max() < 65504  # of the output's range
+    check(o, lse, want, mask)
+    assert q.device_errors() == 0
