@@ -12,13 +12,14 @@
 //   2. V: the row as RN_fp16(s q + b) (what qmm_dequantize gives); where that passes fp16's range, 2^-5 times it,
 //      and the position's P 2^5 times.
 //   3. A softmax thread reads its position's sums: x = f * (bias + sum over groups of s * sum) - ref, all
-//      fp32 (the product rounded before ref comes off, so that the largest x is 0 however large the scores
-//      are), P = 2^x, and keeps its share of the rows' sums l in registers; P goes to shared memory as
+//      fp32 (the product rounded before ref comes off, so that the largest x lies between 0 and 8 however large
+//      the scores are), P = 2^x, and keeps its share of the rows' sums l in registers; P goes to shared memory as
 //      fp16 (for fp16 outputs as two terms, so that V's rounding is the only one before the output's).
 //   4. O^T += V^T P: V's rows as they are stored are the transposed (MN-major) operand, and so is P.
 //
-// References are moved only when some x passes 14 (fp16 holds P up to 2^15): then by the largest x of
-// the tile (redux over the warps' lanes), with O rescaled in tensor memory.  K of the next tile is converted and
+// References are moved only when some x passes 15 (fp16 holds P up to 2^16): then so that the largest x of the
+// tile is 8 (redux over the warps' lanes), with O rescaled in tensor memory; fp16 is exact to 2^-11 down to 2^-22
+// of the largest P (100,000 positions of 2^-23.4 each lost a third of their part with it at 1).  K of the next tile is converted and
 // its scores are under way while this tile's softmax runs; two blocks an SM fill what waits are left.
 // 1,024 tokens of 32 heads over 8,191 positions of 128: 405 us, 0.32 PFLOP/s; bound by the two warpgroups'
 // waits for each other (issue slots 43% busy, tensor pipe 16%), not by the MMAs.
@@ -38,7 +39,7 @@ __device__ unsigned g_tc_attn_errors;  // bit 0: a wait ran out; bit 1: a page o
 
 constexpr int kPos = kAttnTcUnit;          // positions a tile
 constexpr int kTcThreads = 2 * kPos;       // a warpgroup for the softmax, one for the conversions
-constexpr float kMaxX = 14.f;
+constexpr float kMaxX = 15.f, kAimX = 8.f;  // where references move, and what the largest x is then
 constexpr int kRegsS = 152, kRegsC = 104;  // registers a thread of the two, of 128 each at the launch: their sum is 256
 
 template <int D, int GRP, int N>
@@ -582,7 +583,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                         if (tid < HR) {  // the factor of what there is, in red's first row
                             const int r = h0 + tid;
                             const float was = -nref[r];
-                            const float now = fmaxf(was, fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])));
+                            // rounded up: x stays below kAimX however large the scores are
+                            const float now = fmaxf(was, __fadd_ru(fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r])), -kAimX));
                             red[r] = ex2(was - now);
                             nref[r] = -now;
                         }
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_tc_kernel(const __grid_con
                 } else if (a.lse != nullptr) {
                     const int qr = cur->row_lo + tid, tok = qr / a.group_heads;
                     a.lse[int64_t(cur->row0 + tok) * (a.kv_heads * a.group_heads) + cur->h * a.group_heads + qr - tok * a.group_heads] =
-                        ls == 0.f ? -INFINITY : (lg2(ls) - nref[tid]) * 0.693147180559945309f;
+                        lse_of(-nref[tid], ls);
                 }
             }
             group_sync(2);
