@@ -1110,38 +1110,74 @@ size_t sk_smem(int bits, int mp, int sc, int xslots) {
 // order, so they can share it; calls on different streams (or in different captured
 // graphs) never do.  The arrival words carry the tag of the call that last used them and
 // are reset by the last block to arrive, so the memory needs no clearing.
+//
+// Streams are told apart by their ids, not by their handles: cudaStreamPerThread is one handle for
+// a different stream in each host thread, and the handle of a destroyed stream, whose work may still be
+// running, may come back for a new one.  When that happens the old one's memory is freed, which waits for its work.
 namespace {
 struct WsKey {
     int dev;
-    uintptr_t stream;
-    unsigned long long capture;
+    unsigned long long stream, capture;
     bool operator==(const WsKey& o) const { return dev == o.dev && stream == o.stream && capture == o.capture; }
 };
 struct WsKeyHash {
     size_t operator()(const WsKey& k) const {
-        return std::hash<uintptr_t>()(k.stream) ^ (std::hash<unsigned long long>()(k.capture) * 31) ^ size_t(k.dev);
+        return std::hash<unsigned long long>()(k.stream * 64 + unsigned(k.dev)) ^ (std::hash<unsigned long long>()(k.capture) * 31);
     }
 };
 struct Ws {
     void* ptr;
     size_t bytes;
 };
+using WsMap = std::unordered_map<WsKey, Ws, WsKeyHash>;
 
 std::mutex g_ws_mu;
-std::unordered_map<WsKey, Ws, WsKeyHash> g_ws;
+WsMap g_ws, g_counters;
+std::unordered_map<uintptr_t, unsigned long long> g_ws_ids[64];  // by device: the stream that a handle was last
 std::vector<void*> g_ws_retired;  // outgrown workspaces: kernels in flight may still use them
 
-}  // namespace
-
-cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+cudaError_t ws_key(cudaStream_t stream, WsKey* key) {
+    cudaError_t e = cudaGetDevice(&key->dev);
     if (e != cudaSuccess) return e;
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
     unsigned long long cid = 0;
     e = cudaStreamGetCaptureInfo(stream, &st, &cid);
     if (e != cudaSuccess) return e;
-    const WsKey key{dev, reinterpret_cast<uintptr_t>(stream), st == cudaStreamCaptureStatusActive ? cid : 0ull};
+    key->capture = st == cudaStreamCaptureStatusActive ? cid : 0ull;
+    if (key->capture) {  // a capture's number is its own, and asking a capturing stream for its id ends the capture
+        static thread_local char mine;
+        key->stream = reinterpret_cast<uintptr_t>(stream == cudaStreamPerThread ? static_cast<void*>(&mine) : stream);
+        return cudaSuccess;
+    }
+    // relaxed rules for the question: another thread's capture may be in progress
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamGetId(stream, &key->stream);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return e;
+}
+
+// A stream's first call outside captures: if its handle was another stream's, that one's memory is freed.
+void ws_handle(cudaStream_t stream, const WsKey& key) {
+    if (stream == cudaStreamPerThread || key.capture || key.dev >= 64) return;
+    auto was = g_ws_ids[key.dev].emplace(reinterpret_cast<uintptr_t>(stream), key.stream).first;
+    if (was->second == key.stream) return;
+    for (WsMap* all : {&g_ws, &g_counters}) {
+        auto it = all->find(WsKey{key.dev, was->second, 0});
+        if (it == all->end()) continue;
+        cudaFree(it->second.ptr);
+        all->erase(it);
+    }
+    was->second = key.stream;
+}
+
+}  // namespace
+
+cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out) {
+    WsKey key;
+    cudaError_t e = ws_key(stream, &key);
+    if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(g_ws_mu);
     auto it = g_ws.find(key);
     if (it != g_ws.end() && it->second.bytes >= bytes) {
@@ -1155,6 +1191,7 @@ cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out) {
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     e = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
+    if (it == g_ws.end()) ws_handle(stream, key);
     void* ptr = nullptr;
     e = cudaMalloc(&ptr, want);
     cudaThreadExchangeStreamCaptureMode(&mode);
@@ -1170,37 +1207,33 @@ cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out) {
 }
 
 cudaError_t arrival_counters(cudaStream_t stream, unsigned** out) {
-    static std::unordered_map<WsKey, unsigned*, WsKeyHash> all;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    WsKey key;
+    cudaError_t e = ws_key(stream, &key);
     if (e != cudaSuccess) return e;
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    unsigned long long cid = 0;
-    e = cudaStreamGetCaptureInfo(stream, &st, &cid);
-    if (e != cudaSuccess) return e;
-    const WsKey key{dev, reinterpret_cast<uintptr_t>(stream), st == cudaStreamCaptureStatusActive ? cid : 0ull};
     std::lock_guard<std::mutex> lk(g_ws_mu);
-    auto it = all.find(key);
-    if (it != all.end()) {
-        *out = it->second;
+    auto it = g_counters.find(key);
+    if (it != g_counters.end()) {
+        *out = static_cast<unsigned*>(it->second.ptr);
         return cudaSuccess;
     }
     // as in split_workspace; the zeros are written by a stream of its own, once
+    constexpr size_t bytes = kArrivalCounters * sizeof(unsigned);
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     e = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
+    ws_handle(stream, key);
     void* ptr = nullptr;
     cudaStream_t own = nullptr;
-    e = cudaMalloc(&ptr, kArrivalCounters * sizeof(unsigned));
+    e = cudaMalloc(&ptr, bytes);
     if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
-    if (e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, kArrivalCounters * sizeof(unsigned), own);
+    if (e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, bytes, own);
     if (e == cudaSuccess) e = cudaStreamSynchronize(own);
     if (own) cudaStreamDestroy(own);
     if (e != cudaSuccess && ptr) cudaFree(ptr);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
     *out = static_cast<unsigned*>(ptr);
-    all.emplace(key, *out);
+    g_counters.emplace(key, Ws{ptr, bytes});
     return cudaSuccess;
 }
 
