@@ -13,6 +13,12 @@ pytestmark = pytest.mark.gpu
 PER_THREAD = 2  # cudaStreamPerThread: one handle, a stream for each host thread
 
 
+def finish():
+    """Waits for the calling thread's default stream.  A thread that ends with work pending there can leave the
+    driver spinning for ever (580.159; seen with the GPU idle)."""
+    assert ctypes.CDLL("libcuda.so.1").cuStreamSynchronize(ctypes.c_void_p(PER_THREAD)) == 0
+
+
 def call(c, x, table, lens, cu, out, lse, stream):
     """qmm_kv_attention through the C ABI on any stream handle (the call itself runs without the interpreter's lock)."""
     T, H, D = x.shape
@@ -47,6 +53,7 @@ def test_threads_on_their_own_default_streams(new):
             start.wait(60)
             for turn in range(400):
                 call(*cases[i], *outs[i][turn % 8], PER_THREAD)
+            finish()
         except Exception as e:  # noqa: BLE001 - told to the main thread
             failed.append(e)
 
@@ -108,6 +115,7 @@ def test_eager_calls_of_another_thread_while_one_captures():
     want, other_want = q.kv_attention(*case), q.kv_attention(*other)
     out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
     got, failed = [torch.empty_like(t) for t in other_want], []
+    called, captured = threading.Event(), threading.Event()
     torch.cuda.synchronize()
 
     def eager():
@@ -115,16 +123,22 @@ def test_eager_calls_of_another_thread_while_one_captures():
             torch.cuda.set_device(0)
             for _ in range(5):
                 call(*other, *got, PER_THREAD)  # the first of them allocates
+            called.set()
+            assert captured.wait(60)
+            finish()
         except Exception as e:  # noqa: BLE001 - told to the main thread
             failed.append(e)
+            called.set()
 
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         q.kv_attention(*case, out=out, lse=lse)
         t = threading.Thread(target=eager)
         t.start()
-        t.join()
+        assert called.wait(60)
         q.kv_attention(*case, out=out, lse=lse)
+    captured.set()
+    t.join()
     assert not failed
     g.replay()
     torch.cuda.synchronize()
