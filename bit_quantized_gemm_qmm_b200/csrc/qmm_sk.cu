@@ -1114,6 +1114,8 @@ size_t sk_smem(int bits, int mp, int sc, int xslots) {
 // Streams are told apart by their ids, not by their handles: cudaStreamPerThread is one handle for
 // a different stream in each host thread, and the handle of a destroyed stream, whose work may still be
 // running, may come back for a new one.  When that happens the old one's memory is freed, which waits for its work.
+// A capture's memory belongs to its graph: once that and all its executable graphs are gone, the next
+// call that allocates frees it.
 namespace {
 struct WsKey {
     int dev;
@@ -1135,6 +1137,49 @@ std::mutex g_ws_mu;
 WsMap g_ws, g_counters;
 std::unordered_map<uintptr_t, unsigned long long> g_ws_ids[64];  // by device: the stream that a handle was last
 std::vector<void*> g_ws_retired;  // outgrown workspaces: kernels in flight may still use them
+
+// A captured graph's memory, and the graphs' that are gone (written by the driver's threads, which call nothing).
+struct WsOwned {
+    WsMap* all;
+    WsKey key;
+    void* ptr;
+};
+std::mutex g_gone_mu;
+std::vector<WsOwned*>* const g_gone = new std::vector<WsOwned*>;  // graphs may outlive the library's statics
+void CUDART_CB ws_gone(void* p) {
+    std::lock_guard<std::mutex> lk(g_gone_mu);
+    g_gone->push_back(static_cast<WsOwned*>(p));
+}
+
+// Gives the memory to the graph that the stream is being captured into; without success it is kept for good.
+void ws_give(cudaStream_t stream, WsMap* all, const WsKey& key, void* ptr) {
+    if (!key.capture) return;
+    cudaStreamCaptureStatus st;
+    cudaGraph_t graph = nullptr;
+    if (cudaStreamGetCaptureInfo_v2(stream, &st, nullptr, &graph, nullptr, nullptr) != cudaSuccess || !graph) return;
+    auto* owned = new WsOwned{all, key, ptr};
+    cudaUserObject_t obj;
+    if (cudaUserObjectCreate(&obj, owned, ws_gone, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+        delete owned;
+        return;
+    }
+    cudaGraphRetainUserObject(graph, obj, 1, cudaGraphUserObjectMove);  // on failure the object stays, and with it the memory
+}
+
+// Frees what belonged to graphs that are gone (cudaFree waits for a last replay still in flight).
+void ws_sweep() {
+    std::vector<WsOwned*> gone;
+    {
+        std::lock_guard<std::mutex> lk(g_gone_mu);
+        gone.swap(*g_gone);
+    }
+    for (WsOwned* o : gone) {
+        auto it = o->all->find(o->key);
+        if (it != o->all->end() && it->second.ptr == o->ptr) o->all->erase(it);
+        cudaFree(o->ptr);
+        delete o;
+    }
+}
 
 cudaError_t ws_key(cudaStream_t stream, WsKey* key) {
     cudaError_t e = cudaGetDevice(&key->dev);
@@ -1191,13 +1236,15 @@ cudaError_t split_workspace(cudaStream_t stream, size_t bytes, void** out) {
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     e = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
+    ws_sweep();
     if (it == g_ws.end()) ws_handle(stream, key);
     void* ptr = nullptr;
     e = cudaMalloc(&ptr, want);
+    if (e == cudaSuccess) ws_give(stream, &g_ws, key, ptr);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
     if (it != g_ws.end()) {
-        g_ws_retired.push_back(it->second.ptr);
+        if (!key.capture) g_ws_retired.push_back(it->second.ptr);
         it->second = Ws{ptr, want};
     } else {
         g_ws.emplace(key, Ws{ptr, want});
@@ -1221,6 +1268,7 @@ cudaError_t arrival_counters(cudaStream_t stream, unsigned** out) {
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     e = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
+    ws_sweep();
     ws_handle(stream, key);
     void* ptr = nullptr;
     cudaStream_t own = nullptr;
@@ -1230,6 +1278,7 @@ cudaError_t arrival_counters(cudaStream_t stream, unsigned** out) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(own);
     if (own) cudaStreamDestroy(own);
     if (e != cudaSuccess && ptr) cudaFree(ptr);
+    if (e == cudaSuccess) ws_give(stream, &g_counters, key, ptr);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
     *out = static_cast<unsigned*>(ptr);

@@ -144,3 +144,44 @@ def test_eager_calls_of_another_thread_while_one_captures():
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert torch.equal(got[0], other_want[0]) and torch.equal(got[1], other_want[1])
+
+
+@pytest.mark.parametrize("op", ["attention", "qmm"])
+def test_workspaces_of_graphs_that_are_gone(op):
+    """Graphs captured, replayed and dropped, a last replay in flight: right to the end, and their memory comes back."""
+    if op == "attention":
+        case = long_case(1, 1)
+        want = q.kv_attention(*case)
+        call_one = lambda out: q.kv_attention(*case, out=out[0], lse=out[1])  # noqa: E731
+    else:
+        w = q.QuantizedWeight.from_dense(torch.randn((32000, 1024), device="cuda", generator=gen(1)).half(), 4, 64)
+        x = torch.randn((1, 1024), device="cuda", generator=gen(2)).half()
+        want = (w(x),)
+        call_one = lambda out: w(x, out=out[0])  # noqa: E731
+    outs = [[torch.full_like(t, 7) for t in want] for _ in range(60)]
+    torch.cuda.synchronize()
+    free, kept = [], []
+    for turn, out in enumerate(outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call_one(out)
+        for _ in range(20):
+            g.replay()
+        if turn % 20 == 7:
+            kept.append(g)
+        del g
+        if turn % 20 == 19:
+            free.append(torch.cuda.mem_get_info()[0])
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert free[0] - free[-1] < 60 << 20  # 40 captures' workspaces are 160 MB at least
+    for out in outs:
+        for t in out:
+            t.fill_(7)
+    for g in kept:
+        g.replay()
+    torch.cuda.synchronize()
+    for turn, out in enumerate(outs):
+        if turn % 20 == 7:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
