@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -42,20 +43,24 @@ def _stale(srcs, target) -> bool:
 
 
 def build_call_module(force: bool = False) -> str:
-    """gcc the CPython hand-off module (plain C against the interpreter's headers and torch's dlpack.h)."""
+    """gcc the CPython hand-off module (plain C against the interpreter's headers and, for the K/V cache's calls,
+    torch's dlpack.h)."""
     deps = (CALL_SRC, os.path.join(HERE, "..", "include", "qmm.h"), __file__)
     if not force and os.path.exists(CALL_LIB) and os.path.getmtime(CALL_LIB) >= max(map(os.path.getmtime, deps)):
         return CALL_LIB
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if not cc:
         raise RuntimeError("no C compiler for the _qmm_call module")
-    import torch  # for the place of its headers
-    torch_include = os.path.join(os.path.dirname(torch.__file__), "include")
+    torch = importlib.util.find_spec("torch")  # for the place of its headers
     tmp = CALL_LIB + ".tmp"
-    subprocess.check_call([cc, "-O2", "-shared", "-fPIC", "-Wall", "-Werror",
-                           "-I" + sysconfig.get_paths()["include"], "-I" + torch_include, CALL_SRC, "-o", tmp])
+    subprocess.check_call(call_command(cc, tmp, [os.path.join(d, "include") for d in torch.submodule_search_locations] if torch else []))
     os.replace(tmp, CALL_LIB)
     return CALL_LIB
+
+
+def call_command(cc: str, out: str, includes: list[str]) -> list[str]:
+    return [cc, "-O2", "-shared", "-fPIC", "-Wall", "-Werror", "-I" + sysconfig.get_paths()["include"],
+            *("-I" + d for d in includes), CALL_SRC, "-o", out]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

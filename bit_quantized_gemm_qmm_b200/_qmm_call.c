@@ -12,7 +12,18 @@
 #include <Python.h>
 #include <stdint.h>
 
-#include <ATen/dlpack.h> /* torch's copy of the exchange format: plain C */
+/* torch's copy of the exchange format: plain C.  A torch without the exchange functions gets the module without the
+ * K/V cache's calls. */
+#if defined(__has_include)
+#if __has_include(<ATen/dlpack.h>)
+#include <ATen/dlpack.h>
+#endif
+#endif
+#if defined(DLPACK_MAJOR_VERSION) && DLPACK_MAJOR_VERSION == 1 && DLPACK_MINOR_VERSION >= 3
+#define WITH_KV 1
+#else
+#define WITH_KV 0
+#endif
 
 #include "../include/qmm.h"
 
@@ -62,6 +73,7 @@ static PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     return PyLong_FromLong(st);
 }
 
+#if WITH_KV
 /* ---- the K/V cache: five functions of the ABI, bound together.  They take tensors, read through
  * torch's DLPack exchange functions (a view of a tensor's pointer, sizes and strides in about the
  * time of one attribute look-up), and check what the ABI cannot see. ---- */
@@ -320,16 +332,20 @@ static PyObject* kv_attention(PyObject* self, PyObject* const* args, Py_ssize_t 
                                           args[8] == Py_None ? NULL : (const int64_t*)data(&tree), (qmm_dtype)q.dtype, x.stream));
 }
 
+#endif /* WITH_KV */
+
 static PyMethodDef methods[] = {
     {"bind", bind, METH_O, "bind(address of qmm_ex)"},
     {"qmm_ex", (PyCFunction)(void (*)(void))call, METH_FASTCALL,
      "qmm_ex(x, packed, scales, biases, y, M, N, K, bits, group, dtype, plan, stream) -> status"},
+#if WITH_KV
     {"bind_kv", (PyCFunction)(void (*)(void))bind_kv, METH_FASTCALL, "addresses of the five K/V cache functions, and the tensor type"},
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, "qmm_kv_append -> status"},
     {"kv_gather", (PyCFunction)(void (*)(void))kv_gather, METH_FASTCALL, "qmm_kv_gather -> status"},
     {"kv_copy_pages", (PyCFunction)(void (*)(void))kv_copy_pages, METH_FASTCALL, "qmm_kv_copy_pages -> status"},
     {"kv_compact", (PyCFunction)(void (*)(void))kv_compact, METH_FASTCALL, "qmm_kv_compact -> status"},
     {"kv_attention", (PyCFunction)(void (*)(void))kv_attention, METH_FASTCALL, "qmm_kv_attention -> status"},
+#endif
     {NULL, NULL, 0, NULL},
 };
 

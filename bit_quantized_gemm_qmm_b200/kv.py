@@ -80,6 +80,8 @@ def _calls():
             from . import _qmm_call
         except ImportError as e:
             raise _q.QmmUnavailable(f"the _qmm_call module is missing ({e}); run __graft_entry__.build()") from e
+        if not hasattr(_qmm_call, "bind_kv"):
+            raise _q.QmmUnavailable("the K/V cache needs a torch with DLPack's exchange functions (1.3)")
         _qmm_call.bind_kv(*(ctypes.cast(getattr(L, "qmm_kv_" + n), ctypes.c_void_p).value
                             for n in ("append", "gather", "copy_pages", "compact", "attention")), torch.Tensor)
         _call = _qmm_call
