@@ -212,9 +212,7 @@ class KVSequences:
         """A sequence that begins as a copy of `seq`: full pages shared, the last one copied."""
         pages, n = self._pages[seq], self._lens[seq]
         full = n // self.cache.page_size
-        own = self._take(1) if n % self.cache.page_size else []
-        if own:
-            self._copy(pages[full:full + 1], own)
+        own = self._copies(pages[full:full + 1] if n % self.cache.page_size else [])
         name = self.add()
         for p in pages[:full]:
             self._held[p] += 1
@@ -232,8 +230,16 @@ class KVSequences:
         host = torch.tensor([x for values in lists for x in values], dtype=torch.int32).pin_memory()
         return host.to(self.cache.device, non_blocking=True).split([len(values) for values in lists])
 
-    def _copy(self, src: list[int], dst: list[int]) -> None:
-        kv_copy_pages(self.cache, *self._device(src, dst))
+    def _copies(self, pages: list[int]) -> list[int]:
+        """New pages that are copies of some; none where the copying is refused."""
+        own = self._take(len(pages))
+        try:
+            if own:
+                kv_copy_pages(self.cache, *self._device(pages, own))
+        except Exception:
+            self._drop(own)
+            raise
+        return own
 
     def _table(self, seqs: list[int]):
         """The sequences' page table as one list, and its columns."""
@@ -253,10 +259,8 @@ class KVSequences:
                   if self._held[self._pages[s][i]] > 1]
         if not shared:
             return
-        own = self._take(len(shared))
         was = [self._pages[s][i] for s, i in shared]
-        self._copy(was, own)
-        for (s, i), p in zip(shared, own):
+        for (s, i), p in zip(shared, self._copies(was)):
             self._pages[s][i] = p
         self._drop(was)
 
