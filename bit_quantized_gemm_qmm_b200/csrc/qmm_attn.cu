@@ -795,15 +795,17 @@ cudaError_t launch_attn_blocks(AttnArgs a, void (*fn)(const AttnArgs), int threa
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int head_dim, int group, cudaStream_t stream) {
-    // query rows of a tile: what the sequences have, so that the cache is streamed once wherever they
-    // fit.  Only the average is known here; where several sequences have several tokens, some are
-    // taken to have half as many again (columns that a tile does not fill cost next to nothing)
+    // Query rows of a tile: what the sequences have, so that the cache is streamed once wherever they fit.  Only
+    // the average is known here; where there are several sequences, some are taken to have half as many again.  That
+    // is too many where they are all alike, or their longest is not much longer: 8 sequences of 6 tokens of 4 heads
+    // (24 rows each, taken for 36) run in the tensor-core kernel in 44 us over 4,096 positions and 103 over 16,384,
+    // in three columns of the warps' kernel in 35 and 76; of up to 6 tokens in 28 and 57 against 25 and 49.
+    // It saves 8 of 8 tokens, whose fourth column spills: 45 and 105 us against 58 and 160.
     const int64_t mean = (int64_t(a.tokens) + a.seqs - 1) / a.seqs;
     const int64_t rows = (a.seqs > 1 ? mean + mean / 2 : mean) * a.group_heads;
-    // The warps' kernel up to 32 rows of 128 (it streams the cache once up to there: 8 sequences of 6 tokens of 4
-    // heads over 16k positions take 56 us, the tensor-core kernel 71; 8 of 10 tokens over 4k 48 against 37), up to
-    // 512 of 64, whose two passes over the codes cost half (128 tokens of 4 heads over 8k positions: 56 us against
-    // 70; 16 sequences of 64 tokens over 2k in groups of 32: 85 against 82).  Heads of 256 have only the former
+    // The warps' kernel up to 32 rows (as counted above) of 128, up to 512 of 64, whose two passes over the codes
+    // cost half (128 tokens of 4 heads over 8k positions: 56 us against 70; 16 sequences of 64 tokens over 2k in
+    // groups of 32: 85 against 82).  Heads of 256 have only the former
     const int most_rows = head_dim == 64 ? 512 : 32;
     if (rows > most_rows && attn_tc_supported(head_dim)) return launch_attn_tc(a, int(rows < 65536 ? rows : 65536), head_dim, group, stream);
     const int64_t cols = (rows + 7) / 8, most = head_dim == 256 ? 2 : 4;

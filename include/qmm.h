@@ -370,14 +370,17 @@ qmm_status qmm_kv_compact(const qmm_kv_cache* cache, const qmm_kv_seqs* seqs, co
  *          its sequence's new tokens and, of those, number j if bit j of its mask is set (those
  *          past 64 are not seen).  Not together with a window.
  * A row that sees nothing is zeros with lse = -infinity.  What a row does not see has no part
- * in it, NaN included.  Arithmetic: K's codes enter the tensor cores exactly, q as fp16 relative to
- * its row's largest value (exact unless 2^-24 below it); scores, softmax and sums are fp32; o is
- * rounded once.  Up to 32 query rows a K/V head (new tokens times query heads; 512 at head_dim 64,
- * any number at 256) V's codes are exact too and each probability times V's scale is rounded once to
- * fp16 (by 2^-11, or below 2^-24 of the row's largest such product over all groups by 2^-35 of that);
- * above, V is rounded to the 11 bits of fp16, past its range too, and probabilities are fp16 for bf16
- * outputs and two fp16 terms for fp16 outputs.  Which of the two runs goes by tokens / seqs, not by the
- * lengths.  Results do not depend on timing.
+ * in it, NaN included; an infinity or NaN in a group of V that it sees makes that group of o no number,
+ * and nothing else.  Arithmetic: K's codes enter the tensor cores exactly, q as fp16 relative to its
+ * row's largest value (exact unless 2^-24 below it); scores, softmax and sums are fp32; o is rounded
+ * once.  Two kernels, by the query rows of a K/V head: tokens / seqs, rounded up and, where seqs > 1,
+ * half as many again, rounded down, times the query heads that share it.  Up to 32 of them (512 at
+ * head_dim 64, any number at 256) V's codes are exact too, and each probability times V's scale is
+ * rounded once to fp16: by 2^-11, or below 2^-24 of the row's largest such product over all groups by
+ * 2^-35 of that.  Above, V is rounded to the 11 bits of fp16 (past its range too), and probabilities to
+ * one fp16 term for bf16 outputs and two for fp16 outputs: by 2^-11 (2^-22), or below 2^-22 of the row's
+ * largest by 2^-33 of that.  So a sequence's rounding goes by the whole call's tokens.  Results do not
+ * depend on timing.
  * Uses the stream's workspace (as qmm), a captured call one of its capture: two instances of one
  * captured graph must not run at once.  The tiles of 8 query rows or more that the new tokens make,
  * times kv_heads, times max_pages * page_size / 32, must stay below 2^29.
