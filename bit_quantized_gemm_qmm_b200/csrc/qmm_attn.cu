@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                 }
             }
             {
-                float sums[SUBS][COLS][4];
+                float sums[SUBS][COLS][4], low[MASKED ? SUBS : 1][MASKED ? COLS : 1][4];
                 uint32_t kw[SUBS][4];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
@@ -445,21 +445,34 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                         if (ch % 2 == 0) ldsm_x4(st + swz(kAttnSub * (h0 + u) + krow, ch + kch), kw[u]);
                         const uint32_t w0 = kw[u][2 * (ch & 1)], w1 = kw[u][2 * (ch & 1) + 1];
                         const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
-                        const uint32_t e0 = w0 & 0x000F000Fu, e1 = w1 & 0x000F000Fu, e2 = y0 & 0x000F000Fu, e3 = y1 & 0x000F000Fu;
+                        // The MMA aligns products by the exponents' fields, where a subnormal's is 2^-14 whatever its
+                        // value: beside q's largest, products below 2^-15 (codes in place) or 2^-19 (one place up) are cut
+                        // off.  Where few positions may be seen all codes go one place up, the shifted ones summed apart
+                        constexpr uint32_t me = MASKED ? 0x00F000F0u : 0x000F000Fu;
+                        constexpr int up = MASKED ? 4 : 0;
+                        const uint32_t e0 = (w0 << up) & me, e1 = (w1 << up) & me, e2 = (y0 << up) & me, e3 = (y1 << up) & me;
                         const uint32_t f0 = w0 & 0x00F000F0u, f1 = w1 & 0x00F000F0u, f2 = y0 & 0x00F000F0u, f3 = y1 & 0x00F000F0u;
 #pragma unroll
                         for (int nt = 0; nt < COLS; ++nt) {
                             const uint4 q = NT == 1 ? qreg[NT == 1 ? ch : 0] : q_frag(nt, ch);
-                            if (ch * 32 % GRP == 0) mma_16816_z(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
-                            else mma_16816(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
-                            mma_16816(sums[u][nt], f0, f1, f2, f3, q.z, q.w);
+                            if constexpr (MASKED) {
+                                if (ch * 32 % GRP == 0) mma_16816_z(low[u][nt], e0, e1, e2, e3, q.x, q.y), mma_16816_z(sums[u][nt], f0, f1, f2, f3, q.z, q.w);
+                                else mma_16816(low[u][nt], e0, e1, e2, e3, q.x, q.y), mma_16816(sums[u][nt], f0, f1, f2, f3, q.z, q.w);
+                            } else {
+                                if (ch * 32 % GRP == 0) mma_16816_z(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
+                                else mma_16816(sums[u][nt], e0, e1, e2, e3, q.x, q.y);
+                                mma_16816(sums[u][nt], f0, f1, f2, f3, q.z, q.w);
+                            }
                         }
                         if ((ch + 1) * 32 % GRP == 0) {
 #pragma unroll
                             for (int nt = 0; nt < COLS; ++nt)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
+                                {
+                                    if constexpr (MASKED) sums[u][nt][i] = fmaf(low[u][nt][i], 0.0625f, sums[u][nt][i]);
                                     acc[u][nt][i] = fmaf(ks[u][i >> 1][ch * 32 / GRP], sums[u][nt][i], acc[u][nt][i]);
+                                }
                         }
                     }
                 }

@@ -189,3 +189,24 @@ def test_attention_of_v_beyond_fp16(dim, group, grp, new, dtype, mask):
     assert want[0].abs().max() < 65504  # of the output's range
     check(o, lse, want, mask)
     assert q.device_errors() == 0
+
+
+# dim, group, heads a kv head, window, dtype, lens, new
+@pytest.mark.parametrize("dim,group,grp,window,dtype,lens,new", [
+    (128, 64, 3, 0, HF, [1, 2, 3, 2, 1, 2, 1], [1] * 7), (256, 64, 7, 0, HF, [1, 2] * 8, [1] * 16), (64, 64, 16, 3, HF, [1, 2, 4, 3], [1] * 4),
+    (128, 128, 2, 1, HF, [500, 700], [3, 5]), (64, 32, 3, 2, HF, [100, 17, 64, 65], [2] * 4), (256, 32, 4, 2, BF, [300], [40]),
+    (128, 128, 8, 1, HF, [600], [600]), (128, 64, 4, 2, HF, [300, 40], [300, 40]), (64, 32, 16, 1, HF, [200], [200]), (128, 32, 4, 1, HF, [90], [60]),
+    (128, 64, 4, 1, BF, [600], [600]), (128, 64, 4, 2, BF, [90], [20])])
+def test_lse_of_rows_that_see_one_or_two_positions(dim, group, grp, window, dtype, lens, new):
+    """Their lse is the score of a position or two, with nothing to average: as a whole within 2^-21, some eight
+    roundings of fp32 (dot products of up to 256 terms, s q code and b sum(q) several times their sum)."""
+    hk, page = 2, 64
+    need = sum(-(-n // page) for n in lens)
+    c = filled_cache(need, page, hk, dim, group, 7, loud=1.0)
+    table = page_tables(lens, page, need, 8)
+    x = torch.randn((sum(new), hk * grp, dim), device="cuda", generator=gen(9)).to(dtype)
+    cu = ints([sum(new[:i]) for i in range(len(new) + 1)])
+    _, lse = q.kv_attention(c, x, table, ints(lens), cu, window=window)
+    want = ref.attention(c.arrays(), page, x, table, lens, cu.tolist(), dim ** -0.5, window)[1]
+    off = ((lse.double() - want).norm() / want.norm()).item()
+    assert off <= 2.0 ** -21, f"{off:.3g}"
