@@ -34,8 +34,9 @@
 // arrive, in an order that does not depend on timing.
 //
 // Bound by the stream of codes and, nearly as much, by the instructions that take them apart: 32 sequences of
-// up to 16,384 positions (313 MB) take 67 us, 4.7 TB/s, the loop itself 5.9; the rest is the items' starts.  One
-// token over 1,024 positions takes 9 us: the plan, the first tiles and the join, one after another.
+// up to 16,384 positions (313 MB) take 70 us, 4.5 TB/s (issue slots 55% busy, ALU 50%); what is missing is the items'
+// starts and shares that do not end together.  One token over 1,024 positions takes 9 us: the plan, the first tiles
+// and the join, one after another.
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>

@@ -90,7 +90,7 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
 // One thread the same one or two words of K and of V; a group's range is found by the lanes that share it.
 // Two words halve what a thread spends on finding its rows; one is faster while the threads do not fill the
 // GPU (8 heads of 128: 64 tokens 4.0 us against 5.5, 512 tokens 4.4 against 5.8, 8,191 tokens 23.4 against 20.9,
-// which is 2.3 TB/s of bf16 rows in and codes out: the arithmetic of the codes bounds it, not memory).
+// which is 2.1 TB/s of rows in and codes out: issue slots are 65% busy, 24 instructions a value, DRAM 18%).
 // The steps are the scheme of qmm_quant.cu, rounded the same way, so the bits are those of qmm_quantize (its
 // scan keeps the first of equal extremes, which decides the sign of a zero: so does this one).  A group
 // with an infinity or NaN, or whose scale or bias leaves fp16, is stored so that it reads as NaN.
