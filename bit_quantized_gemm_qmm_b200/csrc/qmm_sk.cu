@@ -1114,8 +1114,8 @@ size_t sk_smem(int bits, int mp, int sc, int xslots) {
 // Streams are told apart by their ids, not by their handles: cudaStreamPerThread is one handle for
 // a different stream in each host thread, and the handle of a destroyed stream, whose work may still be
 // running, may come back for a new one.  When that happens the old one's memory is freed, which waits for its work.
-// A capture's memory belongs to its graph: once that and all its executable graphs are gone, the next
-// call that allocates frees it.
+// A capture's memory belongs to its graph, a host thread's default stream's to the thread: once the graph and
+// all its executable graphs are gone, or the thread is, the next call that allocates frees it.
 namespace {
 struct WsKey {
     int dev;
@@ -1138,7 +1138,8 @@ WsMap g_ws, g_counters;
 std::unordered_map<uintptr_t, unsigned long long> g_ws_ids[64];  // by device: the stream that a handle was last
 std::vector<void*> g_ws_retired;  // outgrown workspaces: kernels in flight may still use them
 
-// A captured graph's memory, and the graphs' that are gone (written by the driver's threads, which call nothing).
+// A captured graph's memory (or, without a pointer, what a thread's default stream has), and the memory of those that
+// are gone (written by the driver's threads and by ending ones, which call nothing).
 struct WsOwned {
     WsMap* all;
     WsKey key;
@@ -1150,6 +1151,16 @@ void CUDART_CB ws_gone(void* p) {
     std::lock_guard<std::mutex> lk(g_gone_mu);
     g_gone->push_back(static_cast<WsOwned*>(p));
 }
+
+// The default streams that the calling thread has had memory for, one a device.
+struct WsThread {
+    std::vector<WsKey> keys;
+    ~WsThread() {
+        for (const WsKey& k : keys)
+            for (WsMap* all : {&g_ws, &g_counters}) ws_gone(new WsOwned{all, k, nullptr});
+    }
+};
+thread_local WsThread t_ws;
 
 // Gives the memory to the graph that the stream is being captured into; without success it is kept for good.
 void ws_give(cudaStream_t stream, WsMap* all, const WsKey& key, void* ptr) {
@@ -1166,7 +1177,7 @@ void ws_give(cudaStream_t stream, WsMap* all, const WsKey& key, void* ptr) {
     cudaGraphRetainUserObject(graph, obj, 1, cudaGraphUserObjectMove);  // on failure the object stays, and with it the memory
 }
 
-// Frees what belonged to graphs that are gone (cudaFree waits for a last replay still in flight).
+// Frees what belonged to graphs and threads that are gone (cudaFree waits for what is still in flight).
 void ws_sweep() {
     std::vector<WsOwned*> gone;
     {
@@ -1175,8 +1186,9 @@ void ws_sweep() {
     }
     for (WsOwned* o : gone) {
         auto it = o->all->find(o->key);
-        if (it != o->all->end() && it->second.ptr == o->ptr) o->all->erase(it);
-        cudaFree(o->ptr);
+        const bool kept = it != o->all->end() && (!o->ptr || it->second.ptr == o->ptr);
+        cudaFree(o->ptr ? o->ptr : kept ? it->second.ptr : nullptr);
+        if (kept) o->all->erase(it);
         delete o;
     }
 }
@@ -1203,9 +1215,16 @@ cudaError_t ws_key(cudaStream_t stream, WsKey* key) {
     return e;
 }
 
-// A stream's first call outside captures: if its handle was another stream's, that one's memory is freed.
+// A stream's first call outside captures: if its handle was another stream's, that one's memory is freed; a
+// thread's default stream is noted.
 void ws_handle(cudaStream_t stream, const WsKey& key) {
-    if (stream == cudaStreamPerThread || key.capture || key.dev >= 64) return;
+    if (key.capture || key.dev >= 64) return;
+    if (stream == cudaStreamPerThread) {
+        for (const WsKey& k : t_ws.keys)
+            if (k == key) return;
+        t_ws.keys.push_back(key);
+        return;
+    }
     auto was = g_ws_ids[key.dev].emplace(reinterpret_cast<uintptr_t>(stream), key.stream).first;
     if (was->second == key.stream) return;
     for (WsMap* all : {&g_ws, &g_counters}) {

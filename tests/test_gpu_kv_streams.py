@@ -185,3 +185,33 @@ def test_workspaces_of_graphs_that_are_gone(op):
     for turn, out in enumerate(outs):
         if turn % 20 == 7:
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_workspaces_of_threads_that_are_gone():
+    """Threads come, call on their default streams, wait and end: their workspaces do not pile up."""
+    case = long_case(1, 1)
+    want, wl = q.kv_attention(*case)
+    outs = [(torch.full_like(want, 7), torch.full_like(wl, 7)) for _ in range(60)]
+    torch.cuda.synchronize()
+    free, failed = [], []
+
+    def work(o, l):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(3):
+                call(*case, o, l, PER_THREAD)
+            finish()
+        except Exception as e:  # noqa: BLE001 - told to the main thread
+            failed.append(e)
+
+    for turn, (o, l) in enumerate(outs):
+        t = threading.Thread(target=work, args=(o, l))
+        t.start()
+        t.join()
+        if turn % 20 == 19:
+            free.append(torch.cuda.mem_get_info()[0])
+    torch.cuda.synchronize()
+    assert not failed
+    for o, l in outs:
+        assert torch.equal(o, want) and torch.equal(l, wl)
+    assert free[0] - free[-1] < 60 << 20  # 40 threads' workspaces are 160 MB at least
