@@ -159,7 +159,9 @@ class KVSequences:
 
     Sequences are named by the numbers that ``add`` and ``fork`` return.  Forked sequences share their
     full pages; a partly filled last page is copied when the fork is made.  Pages go back to the pool
-    when the last sequence that holds them lets go.
+    when the last sequence that holds them lets go.  One cache, so one layer: a model has an object a layer.
+    Each step lists its sequences' pages anew on the host (0.4 ms for 32 sequences of 8,192 positions in pages
+    of 64); a loop that is bound by that keeps its own tables and makes the calls itself.
 
         s = KVSequences(cache)
         a = s.add()

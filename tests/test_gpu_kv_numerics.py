@@ -210,3 +210,21 @@ def test_lse_of_rows_that_see_one_or_two_positions(dim, group, grp, window, dtyp
     want = ref.attention(c.arrays(), page, x, table, lens, cu.tolist(), dim ** -0.5, window)[1]
     off = ((lse.double() - want).norm() / want.norm()).item()
     assert off <= 2.0 ** -21, f"{off:.3g}"
+
+
+@pytest.mark.parametrize("dim,group,dtype", [(128, 64, BF), (128, 32, HF), (128, 128, BF), (64, 64, BF)])
+def test_attention_of_decodes_beside_a_chunk(dim, group, dtype):
+    """One long chunk of a prompt makes every sequence of the call many rows' kernel's: single tokens over caches of
+    one position to a thousand, one without new tokens, a short draft."""
+    hk, grp, page = 2, 8 if dim == 128 else 32, 64
+    lens, new = [700, 1, 2, 128, 129, 1000, 300, 64, 37], [300, 1, 1, 1, 1, 1, 0, 1, 5]
+    need = sum(-(-n // page) for n in lens)
+    c = filled_cache(need, page, hk, dim, group, 11)
+    table = page_tables(lens, page, need, 12)
+    x = torch.randn((sum(new), hk * grp, dim), device="cuda", generator=gen(13)).to(dtype)
+    assert ref.many_rows(x, hk, len(lens))
+    cu = ints([sum(new[:i]) for i in range(len(new) + 1)])
+    for window in (0, 50):
+        o, lse = q.kv_attention(c, x, table, ints(lens), cu, window=window)
+        check(o, lse, ref.attention(c.arrays(), page, x, table, lens, cu.tolist(), dim ** -0.5, window), f"window {window}")
+    assert q.device_errors() == 0
