@@ -469,8 +469,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
 #pragma unroll
                             for (int nt = 0; nt < COLS; ++nt)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                {
+                                for (int i = 0; i < 4; ++i) {
                                     if constexpr (MASKED) sums[u][nt][i] = fmaf(low[u][nt][i], 0.0625f, sums[u][nt][i]);
                                     acc[u][nt][i] = fmaf(ks[u][i >> 1][ch * 32 / GRP], sums[u][nt][i], acc[u][nt][i]);
                                 }
@@ -527,7 +526,7 @@ __global__ void __launch_bounds__(32 * AttnFmt<D, GRP, NT>::W, AttnFmt<D, GRP, N
                             most = max3_abs(max3_abs(most, m[0], m[1]), m[2], m[3]);
                         }
                     }
-                return fabsf(most) >= 32768.f || top > 60.f;  // 2^15 is 0x7800
+                return most >= 32768.f || top > 60.f;
             };
             if (__any_sync(kFull, probabilities())) {
                 // New references from these positions: the largest P * s becomes 2^10, or P is 1 where s alone is

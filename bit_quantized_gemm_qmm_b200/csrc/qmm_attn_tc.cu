@@ -19,8 +19,9 @@
 //
 // References are moved only when some x passes 15 (fp16 holds P up to 2^16): then so that the largest x of the
 // tile is 8 (redux over the warps' lanes), with O rescaled in tensor memory; fp16 is exact to 2^-11 down to 2^-22
-// of the largest P (100,000 positions of 2^-23.4 each lost a third of their part with it at 1).  K of the next tile is converted and
-// its scores are under way while this tile's softmax runs; two blocks an SM fill what waits are left.
+// of the largest P (100,000 positions of 2^-23.4 each lost a third of their part with it at 1).
+// K of the next tile is converted and its scores are under way while this tile's softmax runs; two blocks an SM fill
+// what waits are left.
 // 1,024 tokens of 32 heads over 8,191 positions of 128: 412 us, 0.31 PFLOP/s; bound by the two warpgroups'
 // waits for each other (issue slots 44% busy, tensor pipe 16%), not by the MMAs.
 // Every wait on a barrier is bounded; a block whose wait runs out goes through its barriers and says so.
